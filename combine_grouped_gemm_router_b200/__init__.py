@@ -84,6 +84,14 @@ _sigs = {
     "moe_layer_shared": ([_SP, c_i32] + [c_p] * 14 + [c_size, c_p], c_i32),
     "moe_layer": ([_SP] + [c_p] * 11 + [c_size, c_p], c_i32),
     "moe_affinity_accumulate": ([c_i32, c_i32, c_i32, c_p, c_p, c_p, c_p], c_i32),
+    "moe_balance_workspace_size": ([_SP], c_size),
+    "moe_balance_loss": ([_SP] + [c_p] * 3 + [c_f32] * 2 + [c_p] * 5 + [c_size, c_p], c_i32),
+    "moe_balance_loss_backward": ([_SP] + [c_p] * 4 + [c_f32] * 2 + [c_p] * 3, c_i32),
+    "moe_route_backward_workspace_size": ([_SP], c_size),
+    "moe_route_backward": ([_SP] + [c_p] * 12 + [c_size, c_p], c_i32),
+    "moe_checkpoint_bytes": ([_SP], c_size),
+    "moe_expert_up_checkpoint": ([_SP] + [c_p] * 7, c_i32),
+    "moe_swiglu_backward": ([_SP] + [c_p] * 7, c_i32),
     "moe_derive_report": ([_SP, ctypes.POINTER(MoeStats), c_p, c_p, ctypes.POINTER(MoeReport)],
                           c_i32),
     "moe_exchange_schedule": ([c_i32, c_p, c_i32, c_p, c_p, c_p, c_p], c_i32),
@@ -412,6 +420,143 @@ def moe_layer_fp8(shape, x, w_router, bias, w1q, w1_scale, w3q, w3_scale, w2q, w
 def moe_affinity_accumulate(N, E, K, topk_j, topk_j1, counts, stream=None):
     _check(_lib.moe_affinity_accumulate(N, E, K, _ptr(topk_j), _ptr(topk_j1), _ptr(counts),
                                         _stream(stream)), "moe_affinity_accumulate")
+
+
+# ---------------------------------------------------------------- training
+
+def _expect(where, *wanted):
+    """Refuses (MoeError) a tensor the kernels would misread: each of ``wanted`` is (name, tensor,
+    dtypes, least number of elements). None and raw addresses pass."""
+    import torch
+    device = None
+    for name, t, dtypes, least in wanted:
+        if t is None or isinstance(t, int):
+            continue
+        if t.dtype not in dtypes:
+            raise MoeError(1, f"{where}: {name} is {t.dtype}, not {' or '.join(map(str, dtypes))}")
+        if not t.is_cuda:
+            raise MoeError(1, f"{where}: {name} is on {t.device}")
+        if device is None:
+            device = torch.cuda.current_device()
+        if t.get_device() != device:
+            raise MoeError(1, f"{where}: {name} is on {t.device}, the current device is "
+                              f"cuda:{device}")
+        if not t.is_contiguous():
+            raise MoeError(1, f"{where}: {name} is not contiguous")
+        if t.numel() < least:
+            raise MoeError(1, f"{where}: {name} has {t.numel()} elements, {least} are needed")
+
+
+def _dtypes():
+    """Element types by the names the checks use (torch is imported on first use)."""
+    global _DTYPES
+    if _DTYPES is None:
+        import torch
+        _DTYPES = {"f32": (torch.float32,), "i32": (torch.int32,), "bf16": (torch.bfloat16,),
+                   "f16": (torch.float16,), "u8": (torch.uint8,),
+                   "mask": (torch.uint8, torch.bool)}
+    return _DTYPES
+
+
+_DTYPES = None
+
+
+def moe_balance_workspace_size(shape: MoeShape) -> int:
+    return _lib.moe_balance_workspace_size(ctypes.byref(shape))
+
+
+def moe_balance_loss(shape, logits, topk_idx, loss, counts, prob_mean, tokens, token_mask=None,
+                     balance_coef=1.0, z_coef=0.0, ws=None, stream=None):
+    """Balance loss and z-loss of the router: loss [3] = (total, balance, z), the per-expert
+    counts [E], the mean probabilities [E] and the number of counted tokens [1]."""
+    d, N, E = _dtypes(), shape.N, shape.E
+    _expect("moe_balance_loss", ("logits", logits, d["f32"], N * E),
+            ("topk_idx", topk_idx, d["i32"], N * shape.K), ("loss", loss, d["f32"], 3),
+            ("counts", counts, d["i32"], E), ("prob_mean", prob_mean, d["f32"], E),
+            ("tokens", tokens, d["i32"], 1), ("token_mask", token_mask, d["mask"], N))
+    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    _check(_lib.moe_balance_loss(ctypes.byref(shape), _ptr(logits), _ptr(topk_idx),
+                                 _ptr(token_mask), balance_coef, z_coef, _ptr(loss),
+                                 _ptr(counts), _ptr(prob_mean), _ptr(tokens), _ptr(ws), ws_bytes,
+                                 _stream(stream)), "moe_balance_loss")
+
+
+def moe_balance_loss_backward(shape, logits, counts, tokens, dlogits, token_mask=None,
+                              balance_coef=1.0, z_coef=0.0, dloss=None, stream=None):
+    """dlogits [N, E]: the gradient of moe_balance_loss's total (times dloss [1], when given)."""
+    d, N, E = _dtypes(), shape.N, shape.E
+    _expect("moe_balance_loss_backward", ("logits", logits, d["f32"], N * E),
+            ("counts", counts, d["i32"], E), ("tokens", tokens, d["i32"], 1),
+            ("dlogits", dlogits, d["f32"], N * E), ("token_mask", token_mask, d["mask"], N),
+            ("dloss", dloss, d["f32"], 1))
+    _check(_lib.moe_balance_loss_backward(ctypes.byref(shape), _ptr(logits), _ptr(token_mask),
+                                          _ptr(counts), _ptr(tokens), balance_coef, z_coef,
+                                          _ptr(dloss), _ptr(dlogits), _stream(stream)),
+           "moe_balance_loss_backward")
+
+
+def moe_route_backward_workspace_size(shape: MoeShape) -> int:
+    return _lib.moe_route_backward_workspace_size(ctypes.byref(shape))
+
+
+def moe_route_backward(shape, x, w_router, dx, dw_router, dbias=None, topk_idx=None, topk_w=None,
+                       dtopk_w=None, dlogits=None, token_mask=None, dx_add=None, ws=None,
+                       stream=None):
+    """Backward pass of moe_route: from the gradients of the gate weights (dtopk_w, with topk_idx
+    and topk_w) and of the logits (dlogits) to dx (fp32, or bf16 with out_bf16), dw_router and
+    dbias."""
+    d, N, E, K = _dtypes(), shape.N, shape.E, shape.K
+    Nd, Ed = N * shape.d, E * shape.d
+    _expect("moe_route_backward", ("x", x, d["bf16"], Nd), ("w_router", w_router, d["f32"], Ed),
+            ("dx", dx, d["bf16" if shape.flags & MOE_FLAG_OUT_BF16 else "f32"], Nd),
+            ("dw_router", dw_router, d["f32"], Ed), ("dbias", dbias, d["f32"], E),
+            ("topk_idx", topk_idx, d["i32"], N * K), ("topk_w", topk_w, d["f32"], N * K),
+            ("dtopk_w", dtopk_w, d["f32"], N * K), ("dlogits", dlogits, d["f32"], N * E),
+            ("token_mask", token_mask, d["mask"], N), ("dx_add", dx_add, d["bf16"], Nd))
+    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    _check(_lib.moe_route_backward(ctypes.byref(shape), _ptr(x), _ptr(w_router), _ptr(topk_idx),
+                                   _ptr(topk_w), _ptr(dtopk_w), _ptr(dlogits), _ptr(token_mask),
+                                   _ptr(dx_add), _ptr(dx), _ptr(dw_router), _ptr(dbias), _ptr(ws),
+                                   ws_bytes, _stream(stream)), "moe_route_backward")
+
+
+def moe_checkpoint_bytes(shape: MoeShape) -> int:
+    """Bytes of the activation checkpoint: rows_alloc rows of checkpoint_stride bytes."""
+    return _lib.moe_checkpoint_bytes(ctypes.byref(shape))
+
+
+def checkpoint_stride(shape: MoeShape) -> int:
+    """Row stride in bytes of the activation checkpoint: f gate codes, f up codes, f / 32 exponents
+    of each, padded to 16."""
+    return 2 * shape.f + (shape.f // 16 + 15) // 16 * 16
+
+
+def moe_expert_up_checkpoint(shape, x_sorted, offsets, w1, w3, h, ckpt, stream=None):
+    """moe_expert_up that also saves the pre-activations in 8 bits (ckpt: moe_checkpoint_bytes
+    of uint8)."""
+    d, rows = _dtypes(), moe_rows_alloc(shape)
+    Efd = shape.E * shape.f * shape.d
+    _expect("moe_expert_up_checkpoint", ("x_sorted", x_sorted, d["bf16"], rows * shape.d),
+            ("offsets", offsets, d["i32"], shape.E + 1), ("w1", w1, d["bf16"], Efd),
+            ("w3", w3, d["bf16"], Efd),
+            ("h", h, d["bf16" if shape.flags & MOE_FLAG_H_BF16 else "f16"], rows * shape.f),
+            ("ckpt", ckpt, d["u8"], rows * checkpoint_stride(shape)))
+    _check(_lib.moe_expert_up_checkpoint(ctypes.byref(shape), _ptr(x_sorted), _ptr(offsets),
+                                         _ptr(w1), _ptr(w3), _ptr(h), _ptr(ckpt),
+                                         _stream(stream)), "moe_expert_up_checkpoint")
+
+
+def moe_swiglu_backward(shape, ckpt, offsets, dh, dgate, dup, h=None, stream=None):
+    """Backward pass of the SwiGLU activation from its 8-bit checkpoint: dgate, dup and (when
+    given) the recomputed h, all bf16, for the rows below offsets[E]."""
+    d, rows = _dtypes(), moe_rows_alloc(shape)
+    n = rows * shape.f
+    _expect("moe_swiglu_backward", ("ckpt", ckpt, d["u8"], rows * checkpoint_stride(shape)),
+            ("offsets", offsets, d["i32"], shape.E + 1), ("dh", dh, d["bf16"], n),
+            ("dgate", dgate, d["bf16"], n), ("dup", dup, d["bf16"], n), ("h", h, d["bf16"], n))
+    _check(_lib.moe_swiglu_backward(ctypes.byref(shape), _ptr(ckpt), _ptr(offsets), _ptr(dh),
+                                    _ptr(dgate), _ptr(dup), _ptr(h), _stream(stream)),
+           "moe_swiglu_backward")
 
 
 # ---------------------------------------------------------------- host helpers

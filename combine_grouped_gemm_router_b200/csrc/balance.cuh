@@ -1,0 +1,359 @@
+// Balance loss of the router with the per-expert counts it rests on, and its gradient.
+//
+// With p_t the softmax of token t's E logits, lse_t their log-sum-exp, M the counted tokens
+// (token_mask != 0), counts[e] the counted assignments to expert e and f_e = counts[e] / (M K):
+//   P_e     = (1/M) sum_t p_te
+//   balance = E sum_e f_e P_e          z = (1/M) sum_t lse_t^2
+//   loss    = cb balance + cz z
+//   dloss/dl_te = p_te (cb E / M (f_e - sum_j f_j p_tj) + cz 2 / M lse_t)
+// (the counts are constants: no gradient passes through the selection).
+//
+// Both passes read the [N][E] logits once. A row is held by LPR lanes, 8 columns each, so the
+// softmax's maximum and sum are log2(LPR) shuffles and a lane owns the same columns in every
+// row it sees: the sums over tokens stay in its registers until the end of the block.
+#pragma once
+
+#include "common.cuh"
+
+namespace moe {
+
+constexpr int kBalThreads = 1024;
+constexpr int kBalCols = 8;  // columns of a row held by one lane
+
+// Lane l of the LPR lanes of a row holds columns col(j), j = 0..7: two 16-byte chunks (VEC,
+// E % 4 == 0) or 8 columns LPR apart. A column at or past E reads as -inf (probability 0).
+template <int LPR, bool VEC>
+struct RowSlice {
+    static __device__ __forceinline__ int col(int l, int j)
+    {
+        return VEC ? 4 * (l + LPR * (j / 4)) + (j & 3) : l + LPR * j;
+    }
+    static __device__ __forceinline__ void load(const float *row, int E, int l, float (&v)[8])
+    {
+        if constexpr (VEC) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int c = 4 * (l + LPR * i);
+                const float4 q = c < E ? *reinterpret_cast<const float4 *>(row + c)
+                                       : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+                v[4 * i] = q.x;
+                v[4 * i + 1] = q.y;
+                v[4 * i + 2] = q.z;
+                v[4 * i + 3] = q.w;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int c = l + LPR * j;
+                v[j] = c < E ? row[c] : -INFINITY;
+            }
+        }
+    }
+    static __device__ __forceinline__ void store(float *row, int E, int l, const float (&v)[8])
+    {
+        if constexpr (VEC) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int c = 4 * (l + LPR * i);
+                if (c < E)
+                    *reinterpret_cast<float4 *>(row + c) =
+                        make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int c = l + LPR * j;
+                if (c < E)
+                    row[c] = v[j];
+            }
+        }
+    }
+};
+
+template <int LPR>
+__device__ __forceinline__ float row_max(float v)
+{
+#pragma unroll
+    for (int off = LPR / 2; off; off >>= 1)
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+    return v;
+}
+template <int LPR>
+__device__ __forceinline__ float row_sum(float v)
+{
+#pragma unroll
+    for (int off = LPR / 2; off; off >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+
+// Softmax of the row in v (in place: exponentials, not yet divided by the returned sum); m the
+// row's maximum.
+template <int LPR>
+__device__ __forceinline__ float row_softmax(float (&v)[8], float &m)
+{
+    m = v[0];
+#pragma unroll
+    for (int j = 1; j < 8; ++j)
+        m = fmaxf(m, v[j]);
+    m = row_max<LPR>(m);
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        v[j] = __expf(v[j] - m);
+        s += v[j];
+    }
+    return row_sum<LPR>(s);
+}
+
+// One block's share of the sums, in the workspace: probability sums [blocks][E], counts
+// [blocks][E], then {sum of lse^2, counted tokens} per block.
+struct BalanceParts {
+    float *prob;
+    int32_t *count;
+    float2 *zm;  // {sum of lse^2, tokens as int bits}
+};
+
+struct BalanceOut {
+    float *loss;         // [3]: loss, balance, z
+    int32_t *counts;     // [E]
+    float *prob_mean;    // [E]
+    int32_t *tokens;     // [1]
+    float cb, cz;
+    int E, K;
+};
+
+// The totals of a whole call -> its outputs. Thread e < E of the block brings expert e's sums.
+__device__ __forceinline__ void balance_outputs(const BalanceOut &o, double prob, int count,
+                                                double z, int tokens, double *red)
+{
+    const int e = threadIdx.x;
+    const double inv_m = tokens > 0 ? 1.0 / tokens : 0.0;
+    double term = 0.0;
+    if (e < o.E) {
+        o.counts[e] = count;
+        o.prob_mean[e] = (float)(prob * inv_m);
+        term = (double)count / o.K * inv_m * (prob * inv_m);
+    }
+    term = warp_sum(term);
+    if ((threadIdx.x & 31) == 0)
+        red[threadIdx.x >> 5] = term;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double bal = 0.0;
+        for (int w = 0; w < (int)(blockDim.x >> 5); ++w)
+            bal += red[w];
+        bal *= o.E;
+        const double zz = z * inv_m;
+        o.loss[0] = (float)(o.cb * bal + o.cz * zz);
+        o.loss[1] = (float)bal;
+        o.loss[2] = (float)zz;
+        o.tokens[0] = tokens;
+    }
+}
+
+// Sums over this block's tokens. SINGLE: the grid is one block, which also writes the outputs.
+template <int LPR, bool VEC, bool SINGLE>
+__global__ void __launch_bounds__(kBalThreads, 1)
+    balance_sums_kernel(const float *__restrict__ logits, const int32_t *__restrict__ topk_idx,
+                        const uint8_t *__restrict__ mask, int N, BalanceParts parts,
+                        BalanceOut out)
+{
+    using Slice = RowSlice<LPR, VEC>;
+    constexpr int GW = 32 / LPR;  // rows of a warp at once
+    constexpr int WARPS = kBalThreads / 32;
+    __shared__ float s_prob[WARPS * LPR * kBalCols];  // 32 warps x up to 256 columns
+    __shared__ int s_count[256];
+    __shared__ float s_z[WARPS];
+    __shared__ int s_m[WARPS];
+    __shared__ double s_red[WARPS];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int l = lane % LPR, grp = lane / LPR;
+    const int E = out.E, K = out.K;
+    if (tid < 256)
+        s_count[tid] = 0;
+    __syncthreads();
+
+    // counts: the block's share of the N*K assignments, in any order (integers)
+    const unsigned NK = (unsigned)N * (unsigned)K;
+    for (unsigned i = blockIdx.x * kBalThreads + tid; i < NK; i += gridDim.x * kBalThreads) {
+        const int e = topk_idx[i];
+        if (mask && !mask[i / (unsigned)K])
+            continue;
+        if ((unsigned)e < (unsigned)E)
+            atomicAdd(&s_count[e], 1);
+        else
+            set_dev_error(MOE_ERR_DEVICE_BOUNDS);
+    }
+
+    float acc[8] = {};
+    float zsum = 0.0f;
+    int m_tok = 0;
+    const int64_t stride = (int64_t)gridDim.x * WARPS * GW;
+    for (int64_t base = ((int64_t)blockIdx.x * WARPS + warp) * GW; base < N; base += stride) {
+        const int64_t t = base + grp;
+        const bool live = t < N && (!mask || mask[t]);
+        float v[8], m;
+        Slice::load(logits + (t < N ? t : 0) * E, live ? E : 0, l, v);
+        if (!live)
+            v[0] = 0.0f;  // keeps the arithmetic of a row left out finite
+        const float s = row_softmax<LPR>(v, m);
+        const float inv = live ? 1.0f / s : 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            acc[j] += v[j] * inv;
+        if (live && l == 0) {
+            const float lse = m + logf(s);
+            if (!isfinite(lse))
+                set_dev_error(MOE_ERR_NONFINITE);
+            zsum += lse * lse;
+            ++m_tok;
+        }
+    }
+
+    // over the row groups of the warp, then over the warps
+#pragma unroll
+    for (int off = LPR; off < 32; off <<= 1) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], off);
+    }
+    if (grp == 0) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            s_prob[warp * (LPR * kBalCols) + Slice::col(l, j)] = acc[j];
+    }
+    zsum = warp_sum(zsum);
+    m_tok = warp_sum(m_tok);
+    if (lane == 0) {
+        s_z[warp] = zsum;
+        s_m[warp] = m_tok;
+    }
+    __syncthreads();
+    float p = 0.0f;
+    if (tid < E) {
+#pragma unroll 8
+        for (int w = 0; w < WARPS; ++w)
+            p += s_prob[w * (LPR * kBalCols) + tid];
+    }
+    float z = 0.0f;
+    int mt = 0;
+    if (tid == 0 || SINGLE) {
+        for (int w = 0; w < WARPS; ++w) {
+            z += s_z[w];
+            mt += s_m[w];
+        }
+    }
+    if constexpr (SINGLE) {
+        balance_outputs(out, p, tid < E ? s_count[tid] : 0, z, mt, s_red);
+    } else {
+        if (tid < E) {
+            parts.prob[(size_t)blockIdx.x * E + tid] = p;
+            parts.count[(size_t)blockIdx.x * E + tid] = s_count[tid];
+        }
+        if (tid == 0)
+            parts.zm[blockIdx.x] = make_float2(z, __int_as_float(mt));
+    }
+}
+
+// Adds up the blocks' shares, in block order within each of the threads of a column.
+__global__ void __launch_bounds__(kBalThreads, 1)
+    balance_finish_kernel(BalanceParts parts, int blocks, BalanceOut out)
+{
+    __shared__ double s_prob[kBalThreads];
+    __shared__ int s_count[kBalThreads];
+    __shared__ double s_red[32];
+    __shared__ double s_z;
+    __shared__ int s_m;
+    const int tid = threadIdx.x, E = out.E;
+    int ep = 1;
+    while (ep < E)
+        ep <<= 1;
+    const int e = tid & (ep - 1), part = tid / ep, np = kBalThreads / ep;
+    double p = 0.0;
+    int c = 0;
+    if (e < E) {
+#pragma unroll 8
+        for (int b = part; b < blocks; b += np) {
+            p += parts.prob[(size_t)b * E + e];
+            c += parts.count[(size_t)b * E + e];
+        }
+    }
+    s_prob[tid] = p;
+    s_count[tid] = c;
+    if (tid < 32) {
+        double z = 0.0;
+        int mt = 0;
+        for (int b = tid; b < blocks; b += 32) {
+            const float2 q = parts.zm[b];
+            z += q.x;
+            mt += __float_as_int(q.y);
+        }
+        z = warp_sum(z);
+        mt = warp_sum(mt);
+        if (tid == 0) {
+            s_z = z;
+            s_m = mt;
+        }
+    }
+    __syncthreads();
+    p = 0.0;
+    c = 0;
+    if (tid < E) {
+        for (int q = 0; q < np; ++q) {
+            p += s_prob[q * ep + tid];
+            c += s_count[q * ep + tid];
+        }
+    }
+    balance_outputs(out, p, c, s_z, s_m, s_red);
+}
+
+// dlogits from the logits, the counts and the number of counted tokens.
+template <int LPR, bool VEC>
+__global__ void __launch_bounds__(256)
+    balance_grad_kernel(const float *logits, const uint8_t *__restrict__ mask,
+                        const int32_t *__restrict__ counts, const int32_t *__restrict__ tokens,
+                        const float *__restrict__ dloss, int N, int E, int K, float cb, float cz,
+                        float *dlogits)
+{
+    using Slice = RowSlice<LPR, VEC>;
+    constexpr int GW = 32 / LPR;
+    const int warp = (blockIdx.x * 256 + threadIdx.x) >> 5, lane = threadIdx.x & 31;
+    const int l = lane % LPR, grp = lane / LPR;
+    const int M = tokens[0];
+    const float inv_m = M > 0 ? 1.0f / (float)M : 0.0f;
+    const float scale = (dloss ? dloss[0] : 1.0f) * inv_m;
+    const float a = scale * cb * (float)E, b = scale * cz * 2.0f;
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int c = Slice::col(l, j);
+        f[j] = c < E ? (float)counts[c] * inv_m / (float)K : 0.0f;
+    }
+    const int64_t stride = (int64_t)(gridDim.x * 256 / 32) * GW;
+    for (int64_t base = (int64_t)warp * GW; base < N; base += stride) {
+        const int64_t t = base + grp;
+        const bool live = t < N && (!mask || mask[t]);
+        float v[8], m;
+        Slice::load(logits + (t < N ? t : 0) * E, live ? E : 0, l, v);
+        if (!live)
+            v[0] = 0.0f;
+        const float s = row_softmax<LPR>(v, m);
+        float dot = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            dot += f[j] * v[j];
+        dot = row_sum<LPR>(dot);
+        const float inv = 1.0f / s;
+        const float inner = dot * inv, lterm = b * (m + logf(s));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float p = v[j] * inv;
+            v[j] = live ? p * (a * (f[j] - inner) + lterm) : 0.0f;
+        }
+        if (t < N)
+            Slice::store(dlogits + t * E, E, l, v);
+    }
+}
+
+}  // namespace moe

@@ -35,6 +35,8 @@
 // 128 K elements instead of 64, so tiles, stages and descriptors keep their byte
 // layout; the epilogue multiplies the accumulator by the row's scale and the
 // output channel's scale (both powers of two, so the products are exact).
+// Mode 4: mode 0 whose epilogue also leaves the pre-activations g and u in the 8-bit
+// checkpoint that the activation's backward pass reads (checkpoint.cuh).
 //
 // Every mbarrier wait is bounded (globaltimer); a wait that runs out records
 // MOE_ERR_DEVICE_TIMEOUT, raises a CTA-wide abort flag, and every role drains
@@ -55,8 +57,10 @@ constexpr uint32_t TMEM_COLS = 512;
 constexpr int THREADS = 192;
 
 // K elements in one 128-byte swizzle atom: 64 bf16 or 128 e4m3.
-__host__ __device__ constexpr bool is_e4m3(int MODE) { return MODE >= 2; }
-__host__ __device__ constexpr bool is_gate(int MODE) { return MODE == 0 || MODE == 2; }
+__host__ __device__ constexpr bool is_e4m3(int MODE) { return MODE == 2 || MODE == 3; }
+__host__ __device__ constexpr bool is_gate(int MODE) { return MODE == 0 || MODE == 2 || MODE == 4; }
+// Gate/up on bf16 operands: the modes whose h may be fp16 (with the range record).
+__host__ __device__ constexpr bool is_gate16(int MODE) { return MODE == 0 || MODE == 4; }
 __host__ __device__ constexpr int atom_k(int MODE) { return is_e4m3(MODE) ? 128 : 64; }
 
 struct Args {
@@ -86,6 +90,8 @@ struct Args {
     // multiplies its accumulators by 2^k (powers of two: both exact).
     uint32_t *h_amax;
     int h_pass;
+    uint8_t *ckpt;       // mode 4: checkpoint rows [rows_alloc][ckpt_stride]
+    int ckpt_stride;
     uint64_t timeout_ns;
 };
 
@@ -373,7 +379,27 @@ __device__ __forceinline__ void stage_scales(const Args &args, int e, int n, int
 // fastest with the smaller batches).
 __host__ __device__ constexpr int epilogue_cols(int MODE)
 {
-    return MODE == 0 ? 16 : MODE == 1 ? 32 : MODE == 2 ? 32 : 64;
+    return MODE == 0 ? 16 : MODE == 3 ? 64 : 32;
+}
+
+// 32 values -> one block of the 8-bit checkpoint: 32 e4m3 codes at dst, the exponent byte j + 127
+// returned (the FP8 return payload's rule, see down_epilogue_fp8_return).
+__device__ __forceinline__ uint32_t checkpoint_block(const float *f, uint8_t *dst)
+{
+    uint32_t mx = 0;
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+        mx = max(mx, __float_as_uint(f[k]) & 0x7FFFFFFFu);
+    const int j = e4m3_scale_exp(__uint_as_float(mx));
+    const float inv = pow2f(-j);
+    uint32_t p[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        p[k] = pack_e4m3x2(f[4 * k] * inv, f[4 * k + 1] * inv) |
+               (pack_e4m3x2(f[4 * k + 2] * inv, f[4 * k + 3] * inv) << 16);
+    reinterpret_cast<uint4 *>(dst)[0] = make_uint4(p[0], p[1], p[2], p[3]);
+    reinterpret_cast<uint4 *>(dst)[1] = make_uint4(p[4], p[5], p[6], p[7]);
+    return (uint32_t)(j + 127);
 }
 
 // Gate/up epilogue of one thread: accumulator row `row` (TMEM lane of this thread),
@@ -381,7 +407,8 @@ __host__ __device__ constexpr int epilogue_cols(int MODE)
 // The FP8 mode first scales the accumulators by the row scale sx and the staged W1 / W3
 // channel scales ss.
 // hscale: the fp16 range scale 2^-k of a second pass (1 otherwise); hmax: the largest |h| bits
-// this thread stored (fp16 path).
+// this thread stored (fp16 path). Mode 4 takes 32 columns at a time, one block of the checkpoint:
+// a thread holds the whole block of its row, so the block's maximum needs no other thread.
 template <int MODE>
 __device__ __forceinline__ void swiglu_epilogue(const Args &args, uint32_t taddr, int n, int row,
                                                 bool store, float sx, const float *ss,
@@ -390,6 +417,7 @@ __device__ __forceinline__ void swiglu_epilogue(const Args &args, uint32_t taddr
     constexpr int CB = epilogue_cols(MODE);
     uint16_t *orow = reinterpret_cast<uint16_t *>(args.out) + (size_t)row * args.ldo;
     uint4 *dst = reinterpret_cast<uint4 *>(orow + n * 128);
+    uint32_t gexp = 0, uexp = 0;  // mode 4: exponent bytes of the tile's four blocks
 #pragma unroll 1
     for (int c = 0; c < 128; c += CB) {
         uint32_t g[CB], u[CB];
@@ -421,8 +449,13 @@ __device__ __forceinline__ void swiglu_epilogue(const Args &args, uint32_t taddr
                     uf[j + 3] *= sx * b.w;
                 }
             }
+            if constexpr (MODE == 4) {
+                uint8_t *codes = args.ckpt + (size_t)row * args.ckpt_stride + n * 128 + c;
+                gexp |= checkpoint_block(gf, codes) << (c / 4);
+                uexp |= checkpoint_block(uf, codes + args.ldo) << (c / 4);
+            }
             uint32_t p[CB / 2];
-            if (MODE == 0 && args.h_f16) {
+            if (is_gate16(MODE) && args.h_f16) {
 #pragma unroll
                 for (int j = 0; j < CB / 2; ++j) {
                     const float h0 = silu_mul(gf[2 * j], uf[2 * j]) * hscale;
@@ -440,6 +473,13 @@ __device__ __forceinline__ void swiglu_epilogue(const Args &args, uint32_t taddr
 #pragma unroll
             for (int j = 0; j < CB / 8; ++j)
                 dst[c / 8 + j] = make_uint4(p[4 * j], p[4 * j + 1], p[4 * j + 2], p[4 * j + 3]);
+        }
+    }
+    if constexpr (MODE == 4) {
+        if (store) {
+            uint8_t *eb = args.ckpt + (size_t)row * args.ckpt_stride + 2 * args.ldo + n * 4;
+            *reinterpret_cast<uint32_t *>(eb) = gexp;
+            *reinterpret_cast<uint32_t *>(eb + args.ldo / 32) = uexp;
         }
     }
 }
@@ -715,12 +755,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     // fp16 range: the second gate/up pass runs only if the first one's largest |h| is beyond
     // fp16's range; it stores h * 2^-k, and the down projection multiplies y by 2^k
     int hk = 0;
-    if (args.h_f16 && (MODE == 1 || (MODE == 0 && args.h_pass == 1)))
+    if (args.h_f16 && (MODE == 1 || (is_gate16(MODE) && args.h_pass == 1)))
         hk = f16_range_exp(*reinterpret_cast<volatile uint32_t *>(args.h_amax));
-    const bool pass_needed = !(MODE == 0 && args.h_f16 && args.h_pass == 1) || hk > 0;
-    if (MODE == 0 && args.h_pass == 1 && hk < 0 && blockIdx.x == 0 && threadIdx.x == 0)
+    const bool pass_needed = !(is_gate16(MODE) && args.h_f16 && args.h_pass == 1) || hk > 0;
+    if (is_gate16(MODE) && args.h_pass == 1 && hk < 0 && blockIdx.x == 0 && threadIdx.x == 0)
         set_dev_error(MOE_ERR_F16_RANGE);  // a non-finite activation: no scale brings it in
-    const float hscale = (MODE == 0 && args.h_pass == 1 && hk > 0) ? pow2f(-hk) : 1.0f;
+    const float hscale = (is_gate16(MODE) && args.h_pass == 1 && hk > 0) ? pow2f(-hk) : 1.0f;
     const float yscale = (MODE == 1 && hk > 0) ? pow2f(hk) : 1.0f;
     uint32_t hmax = 0;  // largest |h| this thread stored (first gate/up pass)
 
@@ -908,7 +948,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     if (!is_gate(MODE) && warp >= 2 && lane == 0)
         bulk_wait_all();  // this warp's y stores are complete before its shared memory goes
-    if (MODE == 0 && args.h_f16 && args.h_pass == 0 && warp >= 2) {
+    if (is_gate16(MODE) && args.h_f16 && args.h_pass == 0 && warp >= 2) {
 #pragma unroll
         for (int off = 16; off; off >>= 1)
             hmax = max(hmax, __shfl_xor_sync(0xffffffffu, hmax, off));
@@ -1240,7 +1280,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     if (!is_gate(MODE) && warp >= 2 && lane == 0)
         bulk_wait_all();  // this warp's y stores are complete before its shared memory goes
-    if (MODE == 0 && args.h_f16 && warp >= 2) {
+    if (is_gate16(MODE) && args.h_f16 && warp >= 2) {
 #pragma unroll
         for (int off = 16; off; off >>= 1)
             hmax = max(hmax, __shfl_xor_sync(0xffffffffu, hmax, off));

@@ -7,12 +7,15 @@
 #include <map>
 #include <mutex>
 
+#include "balance.cuh"
+#include "checkpoint.cuh"
 #include "combine.cuh"
 #include "common.cuh"
 #include "dispatch.cuh"
 #include "exchange_plan.cuh"
 #include "grouped_gemm.cuh"
 #include "route.cuh"
+#include "route_backward.cuh"
 
 using namespace moe;
 
@@ -825,10 +828,12 @@ bool use_pair_tiles(const moe_shape_t *s, const Geometry &g)
 // tensor map's extent: rows past it read as zeros). `pair` selects the CTA-pair kernel;
 // `f16`: h is written (gate/up) or read together with fp16 W2 (down) as fp16, else bf16;
 // h_amax (f16 only, DEVICE, one word): the largest |h| of the gate/up, which sizes the fp16
-// range scale (a second gate/up pass runs only when it is beyond fp16's range).
+// range scale (a second gate/up pass runs only when it is beyond fp16's range). Mode 4 also
+// writes the checkpoint rows at ckpt.
+template <int MODE>
 moe_status_t gemm_up(int E, int d, int f, int64_t a_rows, bool pair, const uint16_t *a,
                      const int32_t *offsets, const uint16_t *w1, const uint16_t *w3, uint16_t *h,
-                     bool f16, uint32_t *h_amax, cudaStream_t st)
+                     bool f16, uint32_t *h_amax, uint8_t *ckpt, cudaStream_t st)
 {
     CUtensorMap tA, tW1, tW3;
     if (!make_tmap(&tA, a, d, (uint64_t)a_rows) || !make_tmap(&tW1, w1, d, (uint64_t)E * f) ||
@@ -845,24 +850,26 @@ moe_status_t gemm_up(int E, int d, int f, int64_t a_rows, bool pair, const uint1
     args.ldo = f;
     args.h_f16 = f16 ? 1 : 0;
     args.h_amax = h_amax;
+    args.ckpt = ckpt;
+    args.ckpt_stride = checkpoint_stride(f);
     args.timeout_ns = kWaitTimeoutNs;
     args.select = 0;
     if (f16 && cudaMemsetAsync(h_amax, 0, sizeof(uint32_t), st) != cudaSuccess)
         return MOE_ERR_CUDA;
     if (pair) {
         args.select = 1;
-        moe_status_t rc = launch_gemm_pair<0>(tA, tW1, tW3, args, st);
+        moe_status_t rc = launch_gemm_pair<MODE>(tA, tW1, tW3, args, st);
         if (rc != MOE_OK)
             return rc;
         args.select = 2;
     }
-    moe_status_t rc = launch_gemm<0, 256>(tA, tW1, tW3, args, st);
+    moe_status_t rc = launch_gemm<MODE, 256>(tA, tW1, tW3, args, st);
     if (rc != MOE_OK || !f16)
         return rc;
     // the fp16 range pass: every expert again with h scaled into range, only if it is needed
     args.select = 0;
     args.h_pass = 1;
-    return launch_gemm<0, 256>(tA, tW1, tW3, args, st);
+    return launch_gemm<MODE, 256>(tA, tW1, tW3, args, st);
 }
 
 // y_stride > 0: y is the FP8 return payload with that row stride (written by plain stores;
@@ -1012,8 +1019,8 @@ moe_status_t expert_up_impl(const moe_shape_t *s, const Geometry &g, const uint1
                             const int32_t *offsets, const uint16_t *w1, const uint16_t *w3,
                             uint16_t *h, cudaStream_t st)
 {
-    return gemm_up(s->E, s->d, s->f, g.rows_alloc, use_pair_tiles(s, g), x_sorted, offsets, w1,
-                   w3, h, h_is_f16(s), h_range_word(h, g, s->f), st);
+    return gemm_up<0>(s->E, s->d, s->f, g.rows_alloc, use_pair_tiles(s, g), x_sorted, offsets, w1,
+                      w3, h, h_is_f16(s), h_range_word(h, g, s->f), nullptr, st);
 }
 
 moe_status_t expert_down_impl(const moe_shape_t *s, const Geometry &g, const uint16_t *h,
@@ -1049,8 +1056,8 @@ moe_status_t shared_expert_impl(const moe_shape_t *s, int f_s, const uint16_t *x
     const bool pair = s->N >= 768;
     // the fp16 range word lives beside the offsets in the caller's scratch
     uint32_t *amax = reinterpret_cast<uint32_t *>(offsets2 + 4);
-    moe_status_t rc = gemm_up(1, s->d, f_s, s->N, pair, x, offsets2, ws1, ws3, h_s, h_is_f16(s),
-                              amax, st);
+    moe_status_t rc = gemm_up<0>(1, s->d, f_s, s->N, pair, x, offsets2, ws1, ws3, h_s,
+                                 h_is_f16(s), amax, nullptr, st);
     if (rc != MOE_OK)
         return rc;
     return gemm_down(1, s->d, f_s, s->N, pair, h_s, offsets2, ws2, y_s, 0, false, h_is_f16(s), amax,
@@ -1105,6 +1112,161 @@ moe_status_t combine_impl(const moe_shape_t *s, const void *y, const int32_t *ro
     else
         yk == 0 ? go(combine_kernel<false, 0>) : yk == 1 ? go(combine_kernel<false, 1>)
                                                          : go(combine_kernel<false, 2>);
+    return launch_status();
+}
+
+// ---------------------------------------------------------------- training
+
+// Blocks of the balance sums: one per SM, and no more than give each warp a row. One block
+// takes a small call alone (and writes its outputs, without a second kernel).
+constexpr int64_t kBalSingle = 8192;  // logits of a call that one block takes
+
+int balance_blocks(const moe_shape_t *s)
+{
+    if ((int64_t)s->N * s->E <= kBalSingle)
+        return 1;
+    const int64_t want = ((int64_t)s->N + 31) / 32;
+    return (int)(want < num_sms() ? want : num_sms());
+}
+
+struct BalanceLayout {
+    size_t prob, count, zm, total;
+};
+
+// Sized for any device (blocks <= kBalMaxBlocks) and for every call of the shape.
+constexpr int kBalMaxBlocks = 256;
+
+BalanceLayout balance_layout(const moe_shape_t *s)
+{
+    BalanceLayout L;
+    size_t o = 0;
+    L.prob = o;
+    o = align_up(o + (size_t)kBalMaxBlocks * s->E * 4);
+    L.count = o;
+    o = align_up(o + (size_t)kBalMaxBlocks * s->E * 4);
+    L.zm = o;
+    o = align_up(o + (size_t)kBalMaxBlocks * 8);
+    L.total = o;
+    return L;
+}
+
+// go(lanes per row, vector loads) as compile-time constants.
+template <typename F>
+void row_slices(int E, F &&go)
+{
+    auto lanes = [&](auto vec) {
+        using std::integral_constant;
+        if (E <= 8)
+            go(integral_constant<int, 1>{}, vec);
+        else if (E <= 16)
+            go(integral_constant<int, 2>{}, vec);
+        else if (E <= 32)
+            go(integral_constant<int, 4>{}, vec);
+        else if (E <= 64)
+            go(integral_constant<int, 8>{}, vec);
+        else if (E <= 128)
+            go(integral_constant<int, 16>{}, vec);
+        else
+            go(integral_constant<int, 32>{}, vec);
+    };
+    if (E % 4 == 0)
+        lanes(std::true_type{});
+    else
+        lanes(std::false_type{});
+}
+
+moe_status_t balance_loss_impl(const moe_shape_t *s, const float *logits, const int32_t *topk_idx,
+                               const uint8_t *mask, const BalanceOut &out, char *ws,
+                               cudaStream_t st)
+{
+    const BalanceLayout L = balance_layout(s);
+    BalanceParts parts{reinterpret_cast<float *>(ws + L.prob),
+                       reinterpret_cast<int32_t *>(ws + L.count),
+                       reinterpret_cast<float2 *>(ws + L.zm)};
+    int blocks = balance_blocks(s);
+    if (blocks > kBalMaxBlocks)
+        blocks = kBalMaxBlocks;
+    row_slices(s->E, [&](auto lpr, auto vec) {
+        constexpr int LPR = decltype(lpr)::value;
+        constexpr bool VEC = decltype(vec)::value;
+        if (blocks == 1)
+            balance_sums_kernel<LPR, VEC, true>
+                <<<1, kBalThreads, 0, st>>>(logits, topk_idx, mask, s->N, parts, out);
+        else
+            balance_sums_kernel<LPR, VEC, false>
+                <<<blocks, kBalThreads, 0, st>>>(logits, topk_idx, mask, s->N, parts, out);
+    });
+    if (blocks > 1)
+        balance_finish_kernel<<<1, kBalThreads, 0, st>>>(parts, blocks, out);
+    return launch_status();
+}
+
+moe_status_t balance_grad_impl(const moe_shape_t *s, const float *logits, const uint8_t *mask,
+                               const int32_t *counts, const int32_t *tokens, const float *dloss,
+                               float cb, float cz, float *dlogits, cudaStream_t st)
+{
+    row_slices(s->E, [&](auto lpr, auto vec) {
+        constexpr int LPR = decltype(lpr)::value;
+        constexpr bool VEC = decltype(vec)::value;
+        const int64_t rows_per_block = 8 * (32 / LPR);
+        const int64_t want = (s->N + rows_per_block - 1) / rows_per_block;
+        const int64_t most = 8 * (int64_t)num_sms();
+        balance_grad_kernel<LPR, VEC><<<(int)(want < most ? want : most), 256, 0, st>>>(
+            logits, mask, counts, tokens, dloss, s->N, s->E, s->K, cb, cz, dlogits);
+    });
+    return launch_status();
+}
+
+struct RouteBackward {
+    const uint16_t *x;
+    const float *w_router;
+    const int32_t *topk_idx;
+    const float *topk_w, *dtopk_w, *dlogits;
+    const uint8_t *mask;
+    const uint16_t *dx_add;
+    void *dx;
+    float *dw, *dbias;
+};
+
+size_t route_backward_scratch(const moe_shape_t *s)
+{
+    return align_up((size_t)s->N * s->E * 4);
+}
+
+moe_status_t route_backward_impl(const moe_shape_t *s, const RouteBackward &a, char *ws,
+                                 cudaStream_t st)
+{
+    float *dl = reinterpret_cast<float *>(ws);
+    const int N = s->N, d = s->d, E = s->E;
+    const int64_t warps = ((int64_t)N + 7) / 8, most = 8 * (int64_t)num_sms();
+    router_dlogits_kernel<<<(int)(warps < most ? warps : most), 256, 0, st>>>(
+        a.topk_idx, a.topk_w, a.dtopk_w, a.dlogits, a.mask, N, E, s->K, dl);
+    if (a.dx) {
+        const dim3 grid((N + 63) / 64, (d + 63) / 64);
+        if (s->flags & MOE_FLAG_OUT_BF16)
+            router_dx_kernel<true><<<grid, 256, 0, st>>>(dl, a.w_router, a.dx_add, N, d, E, a.dx);
+        else
+            router_dx_kernel<false><<<grid, 256, 0, st>>>(dl, a.w_router, a.dx_add, N, d, E, a.dx);
+    }
+    if (a.dw)
+        router_dw_kernel<<<dim3((d + 63) / 64, (E + 15) / 16), 256, 0, st>>>(dl, a.x, a.mask, N, d,
+                                                                            E, a.dw);
+    if (a.dbias)
+        router_dbias_kernel<<<E, 256, 0, st>>>(dl, N, E, a.dbias);
+    return launch_status();
+}
+
+moe_status_t swiglu_backward_impl(const Geometry &g, int f, const uint8_t *ckpt,
+                                  const int32_t *rows_dev, const uint16_t *dh, uint16_t *dgate,
+                                  uint16_t *dup, uint16_t *h, cudaStream_t st)
+{
+    int tx = 4;  // f / 8 is a multiple of 16
+    while (tx < 8 && (f / 8) % (2 << tx) == 0)
+        ++tx;
+    const int64_t ty = 256 >> tx, want = (g.rows_alloc + ty - 1) / ty;
+    const int64_t most = 8 * (int64_t)num_sms();
+    swiglu_backward_kernel<<<(int)(want < most ? want : most), 256, 0, st>>>(
+        ckpt, rows_dev, (int)g.rows_alloc, f, tx, dh, dgate, dup, h);
     return launch_status();
 }
 
@@ -1531,6 +1693,169 @@ moe_expert_up(const moe_shape_t *shape, const uint16_t *x_sorted, const int32_t 
         return MOE_ERR_MISALIGNED;
     return expert_up_impl(shape, g, x_sorted, offsets, w1, w3, h,
                           reinterpret_cast<cudaStream_t>(stream));
+}
+
+__attribute__((visibility("default"))) size_t moe_checkpoint_bytes(const moe_shape_t *shape)
+{
+    Geometry g;
+    if (check_shape(shape, false, &g) != MOE_OK || shape->f < 128 || shape->f % 128 != 0)
+        return 0;
+    return (size_t)g.rows_alloc * checkpoint_stride(shape->f);
+}
+
+__attribute__((visibility("default"))) moe_status_t
+moe_expert_up_checkpoint(const moe_shape_t *shape, const uint16_t *x_sorted,
+                         const int32_t *offsets, const uint16_t *w1, const uint16_t *w3,
+                         uint16_t *h, uint8_t *ckpt, moe_stream_t stream)
+{
+    Geometry g;
+    moe_status_t rc = check_shape(shape, true, &g);
+    if (rc != MOE_OK)
+        return rc;
+    if (shape->N == 0)
+        return MOE_OK;  // empty batch: nothing to do
+    if (!x_sorted || !offsets || !w1 || !w3 || !h || !ckpt)
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned16(x_sorted) || !aligned16(w1) || !aligned16(w3) || !aligned16(h) ||
+        !aligned16(ckpt) || !aligned4(offsets))
+        return MOE_ERR_MISALIGNED;
+    return gemm_up<4>(shape->E, shape->d, shape->f, g.rows_alloc, use_pair_tiles(shape, g),
+                      x_sorted, offsets, w1, w3, h, h_is_f16(shape),
+                      h_range_word(h, g, shape->f), ckpt, reinterpret_cast<cudaStream_t>(stream));
+}
+
+__attribute__((visibility("default"))) moe_status_t
+moe_swiglu_backward(const moe_shape_t *shape, const uint8_t *ckpt, const int32_t *offsets,
+                    const uint16_t *dh, uint16_t *dgate, uint16_t *dup, uint16_t *h,
+                    moe_stream_t stream)
+{
+    Geometry g;
+    moe_status_t rc = check_shape(shape, false, &g);
+    if (rc != MOE_OK)
+        return rc;
+    if (shape->f < 128 || shape->f % 128 != 0)
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (shape->N == 0)
+        return MOE_OK;  // empty batch: nothing to do
+    if (!ckpt || !offsets || !dh || !dgate || !dup)
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned16(ckpt) || !aligned4(offsets) || !aligned16(dh) || !aligned16(dgate) ||
+        !aligned16(dup) || (h && !aligned16(h)))
+        return MOE_ERR_MISALIGNED;
+    return swiglu_backward_impl(g, shape->f, ckpt, offsets + shape->E, dh, dgate, dup, h,
+                                reinterpret_cast<cudaStream_t>(stream));
+}
+
+__attribute__((visibility("default"))) size_t moe_balance_workspace_size(const moe_shape_t *shape)
+{
+    if (check_shape(shape, false, nullptr) != MOE_OK)
+        return 0;
+    return balance_layout(shape).total;
+}
+
+__attribute__((visibility("default"))) moe_status_t
+moe_balance_loss(const moe_shape_t *shape, const float *logits, const int32_t *topk_idx,
+                 const uint8_t *token_mask, float balance_coef, float z_coef, float *loss,
+                 int32_t *counts, float *prob_mean, int32_t *tokens, void *ws, size_t ws_bytes,
+                 moe_stream_t stream)
+{
+    moe_status_t rc = check_shape(shape, false, nullptr);
+    if (rc != MOE_OK)
+        return rc;
+    if (!isfinite(balance_coef) || !isfinite(z_coef) || !loss || !counts || !prob_mean || !tokens)
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned16(loss) || !aligned4(counts) || !aligned16(prob_mean) || !aligned4(tokens))
+        return MOE_ERR_MISALIGNED;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (shape->N == 0) {  // empty batch: zeros
+        const size_t E = (size_t)shape->E;
+        return cudaMemsetAsync(loss, 0, 12, st) == cudaSuccess &&
+                       cudaMemsetAsync(counts, 0, E * 4, st) == cudaSuccess &&
+                       cudaMemsetAsync(prob_mean, 0, E * 4, st) == cudaSuccess &&
+                       cudaMemsetAsync(tokens, 0, 4, st) == cudaSuccess
+                   ? MOE_OK
+                   : MOE_ERR_CUDA;
+    }
+    if (!logits || !topk_idx)
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned16(logits) || !aligned4(topk_idx))
+        return MOE_ERR_MISALIGNED;
+    if (!ws || ws_bytes < balance_layout(shape).total)
+        return MOE_ERR_WORKSPACE_TOO_SMALL;
+    if (!aligned16(ws))
+        return MOE_ERR_MISALIGNED;
+    const BalanceOut out{loss, counts, prob_mean, tokens, balance_coef, z_coef, shape->E, shape->K};
+    return balance_loss_impl(shape, logits, topk_idx, token_mask, out, static_cast<char *>(ws), st);
+}
+
+__attribute__((visibility("default"))) moe_status_t
+moe_balance_loss_backward(const moe_shape_t *shape, const float *logits, const uint8_t *token_mask,
+                          const int32_t *counts, const int32_t *tokens, float balance_coef,
+                          float z_coef, const float *dloss, float *dlogits, moe_stream_t stream)
+{
+    moe_status_t rc = check_shape(shape, false, nullptr);
+    if (rc != MOE_OK)
+        return rc;
+    if (!isfinite(balance_coef) || !isfinite(z_coef))
+        return MOE_ERR_INVALID_ARG;
+    if (shape->N == 0)
+        return MOE_OK;  // empty batch: nothing to do
+    if (!logits || !counts || !tokens || !dlogits)
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned16(logits) || !aligned4(counts) || !aligned4(tokens) || !aligned16(dlogits) ||
+        (dloss && !aligned4(dloss)))
+        return MOE_ERR_MISALIGNED;
+    return balance_grad_impl(shape, logits, token_mask, counts, tokens, dloss, balance_coef,
+                             z_coef, dlogits, reinterpret_cast<cudaStream_t>(stream));
+}
+
+__attribute__((visibility("default"))) size_t
+moe_route_backward_workspace_size(const moe_shape_t *shape)
+{
+    if (check_shape(shape, false, nullptr) != MOE_OK)
+        return 0;
+    const size_t n = route_backward_scratch(shape);
+    return n ? n : kAlign;
+}
+
+__attribute__((visibility("default"))) moe_status_t
+moe_route_backward(const moe_shape_t *shape, const uint16_t *x, const float *w_router,
+                   const int32_t *topk_idx, const float *topk_w, const float *dtopk_w,
+                   const float *dlogits, const uint8_t *token_mask, const uint16_t *dx_add,
+                   void *dx, float *dw_router, float *dbias, void *ws, size_t ws_bytes,
+                   moe_stream_t stream)
+{
+    moe_status_t rc = check_shape(shape, false, nullptr);
+    if (rc != MOE_OK)
+        return rc;
+    if (!dx && !dw_router && !dbias)
+        return MOE_ERR_INVALID_ARG;
+    if ((dw_router && !aligned16(dw_router)) || (dbias && !aligned4(dbias)))
+        return MOE_ERR_MISALIGNED;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (shape->N == 0) {  // empty batch: no tokens, zero weight gradients
+        const size_t E = (size_t)shape->E;
+        if (dw_router && cudaMemsetAsync(dw_router, 0, E * shape->d * 4, st) != cudaSuccess)
+            return MOE_ERR_CUDA;
+        if (dbias && cudaMemsetAsync(dbias, 0, E * 4, st) != cudaSuccess)
+            return MOE_ERR_CUDA;
+        return MOE_OK;
+    }
+    if ((!dtopk_w && !dlogits) || (dtopk_w && (!topk_idx || !topk_w)) || (dx && !w_router) ||
+        (dw_router && !x))
+        return MOE_ERR_INVALID_ARG;
+    if ((x && !aligned16(x)) || (w_router && !aligned16(w_router)) ||
+        (topk_idx && !aligned4(topk_idx)) || (topk_w && !aligned4(topk_w)) ||
+        (dtopk_w && !aligned4(dtopk_w)) || (dlogits && !aligned16(dlogits)) ||
+        (dx_add && !aligned16(dx_add)) || (dx && !aligned16(dx)))
+        return MOE_ERR_MISALIGNED;
+    if (!ws || ws_bytes < route_backward_scratch(shape))
+        return MOE_ERR_WORKSPACE_TOO_SMALL;
+    if (!aligned16(ws))
+        return MOE_ERR_MISALIGNED;
+    const RouteBackward a{x,          w_router, topk_idx, topk_w, dtopk_w,   dlogits,
+                          token_mask, dx_add,   dx,       dw_router, dbias};
+    return route_backward_impl(shape, a, static_cast<char *>(ws), st);
 }
 
 __attribute__((visibility("default"))) moe_status_t

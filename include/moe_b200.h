@@ -511,6 +511,104 @@ moe_status_t moe_affinity_accumulate(int32_t N, int32_t E, int32_t K, const int3
                                      const int32_t *topk_j1, int64_t *counts,
                                      moe_stream_t stream);
 
+/* ---------------------------------------------------------------- training
+ * What a training step of the layer needs beside its forward stages and library GEMMs: the
+ * router's balance loss with its gradient, the router's backward pass, and the experts'
+ * activation saved in 8 bits and differentiated from there. The pages name none of these steps
+ * (they treat inference); the forms are the ones routers of this kind are trained with.
+ *
+ * A step: moe_route (with logits) -> moe_balance_loss -> moe_dispatch ->
+ * moe_expert_up_checkpoint -> moe_expert_down -> moe_combine; back: dh = dy W2 (a GEMM) ->
+ * moe_swiglu_backward -> GEMMs with dgate, dup, h; moe_balance_loss_backward ->
+ * moe_route_backward.
+ *
+ * token_mask [N] uint8, nullable: a token whose byte is 0 (padding) is left out everywhere; its
+ * logits, gate weights, gradients and row of x may hold anything, NaN included. */
+
+/* Workspace bytes for moe_balance_loss. 0 on an invalid shape. */
+size_t moe_balance_workspace_size(const moe_shape_t *shape);
+
+/* Balance loss of the router, with the per-expert counts. M = counted tokens, p_t = softmax of
+ * token t's E logits, lse_t = their log-sum-exp, sums over counted tokens:
+ *   counts[e]    = assignments (t, k) with topk_idx[t][k] = e (before any drop)
+ *   prob_mean[e] = (1/M) sum_t p_te
+ *   loss[1] = E sum_e counts[e] / (M K) * prob_mean[e]       (1 when perfectly even)
+ *   loss[2] = (1/M) sum_t lse_t^2                            (the router's z-loss)
+ *   loss[0] = balance_coef * loss[1] + z_coef * loss[2]
+ * logits [N][E] fp32 and topk_idx [N][K] as moe_route wrote them. Outputs (DEVICE): loss [3]
+ * fp32, counts [E] int32, prob_mean [E] fp32, tokens [1] int32 = M; all 0 when M = 0.
+ * fp32 softmax, fp32 sums within a thread, fp64 across blocks; the same bits every run.
+ * A logit of -inf has probability 0. A counted token with a NaN or +inf logit (or only -inf)
+ * makes the loss NaN or infinite and sets MOE_ERR_NONFINITE; an entry of topk_idx outside
+ * [0, E) is not counted and sets MOE_ERR_DEVICE_BOUNDS. The coefficients must be finite.
+ * ws: moe_balance_workspace_size bytes, 16-byte aligned, contents irrelevant before and after;
+ * calls that may overlap on the GPU need workspaces of their own. */
+moe_status_t moe_balance_loss(const moe_shape_t *shape, const float *logits,
+                              const int32_t *topk_idx, const uint8_t *token_mask,
+                              float balance_coef, float z_coef, float *loss, int32_t *counts,
+                              float *prob_mean, int32_t *tokens, void *ws, size_t ws_bytes,
+                              moe_stream_t stream);
+
+/* Gradient of loss[0] with respect to the logits (counts are constants):
+ *   dlogits[t][e] = dloss * p_te * (balance_coef * E / M * (f_e - sum_j f_j p_tj)
+ *                                   + z_coef * 2 / M * lse_t),   f_e = counts[e] / (M K)
+ * counts, tokens: DEVICE, as moe_balance_loss wrote them (counts summed over the ranks of a job
+ * are accepted too, with tokens summed alike). dloss: DEVICE fp32 [1], NULL = 1. dlogits [N][E]
+ * fp32, written (0 for a masked token, and everywhere when *tokens = 0); may alias logits. */
+moe_status_t moe_balance_loss_backward(const moe_shape_t *shape, const float *logits,
+                                       const uint8_t *token_mask, const int32_t *counts,
+                                       const int32_t *tokens, float balance_coef, float z_coef,
+                                       const float *dloss, float *dlogits, moe_stream_t stream);
+
+/* Workspace bytes for moe_route_backward. 0 on an invalid shape. */
+size_t moe_route_backward_workspace_size(const moe_shape_t *shape);
+
+/* Backward pass of moe_route. With dl [N][E] the gradient of the logits,
+ *   dl[t][e] = dlogits[t][e] + sum over k with topk_idx[t][k] = e of
+ *              w_k (dw_k - sum_j w_j dw_j),   w = topk_w[t], dw = dtopk_w[t]
+ *   dx[t] = dl[t] Wr (+ dx_add[t])    dw_router[e] = sum_t dl[t][e] x[t]    dbias = sum_t dl[t]
+ * dtopk_w [N][K] fp32 (with topk_idx, topk_w as moe_route wrote them) and dlogits [N][E] fp32
+ * (moe_balance_loss_backward's): either may be NULL, not both. A slot whose gate weight was not
+ * used (dropped) has dw = 0. An index outside [0, E) is left out and sets
+ * MOE_ERR_DEVICE_BOUNDS; an index twice in a token counts twice.
+ * dx [N][d] fp32, or bf16 with MOE_FLAG_OUT_BF16; dx_add [N][d] bf16, nullable (the gradient
+ * that reaches x by other ways; a bf16 dx may alias it); a masked token's dx is dx_add or 0.
+ * dw_router [E][d], dbias [E] fp32. Each of dx (with w_router), dw_router (with x) and dbias
+ * may be NULL, not all three. N = 0 writes zero weight gradients.
+ * ws as for moe_balance_loss, moe_route_backward_workspace_size bytes. */
+moe_status_t moe_route_backward(const moe_shape_t *shape, const uint16_t *x,
+                                const float *w_router, const int32_t *topk_idx,
+                                const float *topk_w, const float *dtopk_w, const float *dlogits,
+                                const uint8_t *token_mask, const uint16_t *dx_add, void *dx,
+                                float *dw_router, float *dbias, void *ws, size_t ws_bytes,
+                                moe_stream_t stream);
+
+/* Bytes of the checkpoint buffer: rows_alloc * (2f + roundup16(f / 16)). 0 on an invalid shape
+ * (f % 128 == 0 is needed). */
+size_t moe_checkpoint_bytes(const moe_shape_t *shape);
+
+/* moe_expert_up that also saves what the activation's backward pass needs, in 8 bits: for every
+ * kept row r, g = x_sorted[r] W1[e]^T and u = x_sorted[r] W3[e]^T (fp32 accumulators) as e4m3
+ * codes with one power of two per 32 columns, the block rule of MOE_FLAG_FP8_RETURN. Row r of
+ * ckpt (stride 2f + roundup16(f / 16) bytes): f codes of g, f codes of u, f / 32 exponent bytes
+ * j + 127 of g, f / 32 of u; padding bytes and rows past offsets[E] are left as they were.
+ * h is moe_expert_up's, bit for bit. */
+moe_status_t moe_expert_up_checkpoint(const moe_shape_t *shape, const uint16_t *x_sorted,
+                                      const int32_t *offsets, const uint16_t *w1,
+                                      const uint16_t *w3, uint16_t *h, uint8_t *ckpt,
+                                      moe_stream_t stream);
+
+/* Backward pass of h = silu(g) * u from the checkpoint: with g, u the decoded values, dh the
+ * gradient of h and s = 1 / (1 + e^-g),
+ *   dgate = dh u s (1 + g (1 - s))    dup = dh g s    h = g s u (recomputed; NULL: not wanted)
+ * for the rows below offsets[E] (DEVICE int32; rows past it are neither read nor written).
+ * dh, dgate, dup, h [rows_alloc][f] bf16; fp32 arithmetic, each result rounded once. dgate,
+ * dup or h may alias dh. The recomputed h is bf16 whatever MOE_FLAG_H_BF16 says: it is meant
+ * for the weight gradient dW2 = dy^T h, beside a bf16 dy. Needs f % 128 == 0. */
+moe_status_t moe_swiglu_backward(const moe_shape_t *shape, const uint8_t *ckpt,
+                                 const int32_t *offsets, const uint16_t *dh, uint16_t *dgate,
+                                 uint16_t *dup, uint16_t *h, moe_stream_t stream);
+
 /* ---------------------------------------------------------------- host-side helpers */
 
 /* Derived observability report. HOST pointers: stats (a copy of the device struct),
