@@ -1228,31 +1228,195 @@ struct RouteBackward {
     float *dw, *dbias;
 };
 
-size_t route_backward_scratch(const moe_shape_t *s)
+// Workspace of the router's backward pass.
+struct RouteBackLayout {
+    size_t dl, wp, bias, part, total;
+};
+
+// dWr's tiles: 128 MT columns of x, 128-token chunks, split evenly over G CTAs.
+struct DwGeometry {
+    int ne, mt, tiles, chunks, G, kmax;
+};
+
+DwGeometry dw_geometry(const moe_shape_t *s)
 {
-    return align_up((size_t)s->N * s->E * 4);
+    DwGeometry g;
+    g.ne = (s->E + 63) / 64;
+    // two M tiles share a stage's planes of dl (half the L2 reads of them) while TMEM holds
+    // both accumulators twice
+    g.mt = g.ne <= 2 ? 2 : 1;
+    g.tiles = (s->d + 128 * g.mt - 1) / (128 * g.mt);
+    g.chunks = (s->N + rb::kChunk - 1) / rb::kChunk;
+    const int64_t U = (int64_t)g.tiles * g.chunks;
+    g.G = (int)(U < num_sms() ? U : num_sms());
+    g.kmax = g.G > 0 ? (int)((g.chunks + U / g.G - 1) / (U / g.G)) + 1 : 1;
+    return g;
+}
+
+int split_blocks(const moe_shape_t *s)
+{
+    const int64_t want = ((int64_t)s->N + 15) / 16;
+    const int64_t most = 4 * (int64_t)num_sms();
+    return (int)(want < most ? want : most);
+}
+
+RouteBackLayout route_back_layout(const moe_shape_t *s)
+{
+    RouteBackLayout L;
+    const size_t pitch = ((size_t)s->E + 7) & ~(size_t)7;
+    const DwGeometry g = dw_geometry(s);
+    size_t o = 0;
+    L.dl = o;
+    o = align_up(o + 3 * (size_t)s->N * pitch * 2);
+    L.wp = o;
+    o = align_up(o + 3 * (size_t)s->E * s->d * 2);
+    L.bias = o;
+    o = align_up(o + (size_t)split_blocks(s) * s->E * 4);
+    L.part = o;
+    o = align_up(o + (size_t)g.tiles * g.kmax * s->E * 128 * g.mt * 4);
+    L.total = o;
+    return L;
+}
+
+// Tensor map of `rank` (2 or 3) dimensions, innermost first; pitch: bytes of a row and (3-D)
+// of a plane. Elements outside the extents read as zeros and are not written.
+bool make_tmap_box(CUtensorMap *m, CUtensorMapDataType dt, int rank, const void *ptr,
+                   const cuuint64_t *dims, const cuuint64_t *pitch, const cuuint32_t *box,
+                   CUtensorMapSwizzle swizzle)
+{
+    auto enc = tensor_map_encoder();
+    if (!enc)
+        return false;
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, dt, rank, const_cast<void *>(ptr), dims, pitch, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+moe_status_t launch_router_dx(const moe_shape_t *s, const uint16_t *dl, const uint16_t *wp,
+                              const uint16_t *add, void *dx, cudaStream_t st)
+{
+    const bool bf16 = (s->flags & MOE_FLAG_OUT_BF16) != 0;
+    const cuuint64_t N = (cuuint64_t)s->N, d = (cuuint64_t)s->d, E = (cuuint64_t)s->E;
+    const cuuint64_t pitch = (E + 7) & ~(cuuint64_t)7;
+    CUtensorMap t_dl, t_w, t_dx, t_add;
+    const cuuint64_t dl_dims[3] = {E, N, 3}, dl_pitch[2] = {pitch * 2, N * pitch * 2};
+    const cuuint64_t w_dims[3] = {d, E, 3}, w_pitch[2] = {d * 2, E * d * 2};
+    const cuuint64_t x_dims[2] = {d, N}, dx_pitch[1] = {d * (bf16 ? 2 : 4)}, add_pitch[1] = {d * 2};
+    const cuuint32_t dl_box[3] = {64, 128, 1}, w_box[3] = {64, 64, 1};
+    const cuuint32_t p_box[2] = {(cuuint32_t)(bf16 ? 64 : 32), 32};
+    const CUtensorMapDataType b16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    if (!make_tmap_box(&t_dl, b16, 3, dl, dl_dims, dl_pitch, dl_box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_tmap_box(&t_w, b16, 3, wp, w_dims, w_pitch, w_box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_tmap_box(&t_dx, bf16 ? b16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, dx, x_dims,
+                       dx_pitch, p_box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_tmap_box(&t_add, b16, 2, add ? add : dl, add ? x_dims : dl_dims,
+                       add ? add_pitch : dl_pitch, p_box,
+                       bf16 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+        return MOE_ERR_CUDA;
+    rb::DxArgs a = {};
+    a.N = s->N;
+    a.d = s->d;
+    a.E = s->E;
+    a.chunks = (s->E + 63) / 64;
+    const int planes = bf16 ? 2 : 3;
+    a.bn = 256;
+    while (a.bn > 64 && (planes * a.chunks * (a.bn / 64) * rb::kBox > rb::kDxMaxB ||
+                         a.bn / 2 >= s->d))
+        a.bn /= 2;
+    a.slices = (s->d + a.bn - 1) / a.bn;
+    a.tiles = (s->N + 127) / 128;
+    const int fixed = planes * a.chunks * (a.bn / 64) * rb::kBox + rb::dx_piece_area(bf16) + 1024 +
+                      512;
+    a.units = (rb::kDxMaxSmem - fixed) / rb::kUnit;
+    if (a.units > rb::kDxMaxUnits)
+        a.units = rb::kDxMaxUnits;
+    if (a.units < rb::kDxUnits)
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    a.add = add != nullptr;
+    a.timeout_ns = kWaitTimeoutNs;
+    const int64_t U = (int64_t)a.slices * a.tiles;
+    const int G = (int)(U < num_sms() ? U : num_sms());
+    auto go = [&](auto kern) {
+        if (smem_attr_once(kern, rb::kDxMaxSmem) != cudaSuccess)
+            return MOE_ERR_CUDA;
+        kern<<<G, rb::kDxThreads, fixed + a.units * rb::kUnit, st>>>(t_dl, t_w, t_dx, t_add, a);
+        return launch_status();
+    };
+    return bf16 ? go(rb::router_dx_kernel<true>) : go(rb::router_dx_kernel<false>);
+}
+
+moe_status_t launch_router_dw(const moe_shape_t *s, const DwGeometry &g, const uint16_t *x,
+                              const uint16_t *dl, const uint8_t *mask, float *part,
+                              cudaStream_t st)
+{
+    const cuuint64_t N = (cuuint64_t)s->N, d = (cuuint64_t)s->d, E = (cuuint64_t)s->E;
+    const cuuint64_t pitch = (E + 7) & ~(cuuint64_t)7;
+    CUtensorMap t_x, t_dl;
+    const cuuint64_t x_dims[2] = {d, N}, x_pitch[1] = {d * 2};
+    const cuuint64_t dl_dims[3] = {E, N, 3}, dl_pitch[2] = {pitch * 2, N * pitch * 2};
+    const cuuint32_t x_box[2] = {64, 64}, dl_box[3] = {64, 64, 1};
+    const CUtensorMapDataType b16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    if (!make_tmap_box(&t_x, b16, 2, x, x_dims, x_pitch, x_box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_tmap_box(&t_dl, b16, 3, dl, dl_dims, dl_pitch, dl_box, CU_TENSOR_MAP_SWIZZLE_128B))
+        return MOE_ERR_CUDA;
+    const rb::DwArgs a{s->N, s->d, s->E, g.tiles, g.chunks, g.kmax, mask, part, kWaitTimeoutNs};
+    auto go = [&](auto kern, int smem) {
+        if (smem_attr_once(kern, smem) != cudaSuccess)
+            return MOE_ERR_CUDA;
+        kern<<<g.G, rb::kDwThreads, smem, st>>>(t_x, t_dl, a);
+        return launch_status();
+    };
+    switch (g.ne) {
+    case 1: return go(rb::router_dw_kernel<1, 2>, rb::DwTile<1, 2>::SMEM);
+    case 2: return go(rb::router_dw_kernel<2, 2>, rb::DwTile<2, 2>::SMEM);
+    case 3: return go(rb::router_dw_kernel<3, 1>, rb::DwTile<3, 1>::SMEM);
+    default: return go(rb::router_dw_kernel<4, 1>, rb::DwTile<4, 1>::SMEM);
+    }
 }
 
 moe_status_t route_backward_impl(const moe_shape_t *s, const RouteBackward &a, char *ws,
                                  cudaStream_t st)
 {
-    float *dl = reinterpret_cast<float *>(ws);
-    const int N = s->N, d = s->d, E = s->E;
-    const int64_t warps = ((int64_t)N + 7) / 8, most = 8 * (int64_t)num_sms();
-    router_dlogits_kernel<<<(int)(warps < most ? warps : most), 256, 0, st>>>(
-        a.topk_idx, a.topk_w, a.dtopk_w, a.dlogits, a.mask, N, E, s->K, dl);
+    const RouteBackLayout L = route_back_layout(s);
+    const DwGeometry g = dw_geometry(s);
+    uint16_t *dl = reinterpret_cast<uint16_t *>(ws + L.dl);
+    uint16_t *wp = reinterpret_cast<uint16_t *>(ws + L.wp);
+    float *bias = reinterpret_cast<float *>(ws + L.bias);
+    float *part = reinterpret_cast<float *>(ws + L.part);
+    rb::SplitArgs sa{a.topk_idx, a.topk_w, a.dtopk_w, a.dlogits, a.mask, a.dx ? a.w_router : nullptr,
+                     s->N, s->E, s->K, s->d, (s->E + 7) & ~7, dl, wp, bias, split_blocks(s)};
+    int w_blocks = 0;
     if (a.dx) {
-        const dim3 grid((N + 63) / 64, (d + 63) / 64);
-        if (s->flags & MOE_FLAG_OUT_BF16)
-            router_dx_kernel<true><<<grid, 256, 0, st>>>(dl, a.w_router, a.dx_add, N, d, E, a.dx);
-        else
-            router_dx_kernel<false><<<grid, 256, 0, st>>>(dl, a.w_router, a.dx_add, N, d, E, a.dx);
+        const int64_t want = ((int64_t)s->E * s->d / 8 + rb::kSplitThreads - 1) / rb::kSplitThreads;
+        w_blocks = (int)(want < num_sms() ? want : num_sms());
     }
-    if (a.dw)
-        router_dw_kernel<<<dim3((d + 63) / 64, (E + 15) / 16), 256, 0, st>>>(dl, a.x, a.mask, N, d,
-                                                                            E, a.dw);
-    if (a.dbias)
-        router_dbias_kernel<<<E, 256, 0, st>>>(dl, N, E, a.dbias);
+    row_slices(s->E, [&](auto lpr, auto) {
+        rb::router_split_grad_kernel<decltype(lpr)::value>
+            <<<sa.token_blocks + w_blocks, rb::kSplitThreads, 0, st>>>(sa);
+    });
+    moe_status_t rc = launch_status();
+    if (rc == MOE_OK && a.dx)
+        rc = launch_router_dx(s, dl, wp, a.dx_add, a.dx, st);
+    if (rc == MOE_OK && a.dw)
+        rc = launch_router_dw(s, g, a.x, dl, a.mask, part, st);
+    if (rc != MOE_OK || (!a.dw && !a.dbias))
+        return rc;
+    rb::SumArgs sum = {};
+    sum.d = s->d;
+    sum.E = s->E;
+    sum.tile_cols = 128 * g.mt;
+    sum.tiles = g.tiles;
+    sum.chunks = g.chunks;
+    sum.kmax = g.kmax;
+    sum.G = g.G;
+    sum.part = part;
+    sum.dw = a.dw;
+    sum.dw_blocks = a.dw ? (int)(((int64_t)s->E * s->d / 4 + 255) / 256) : 0;
+    sum.bias_part = bias;
+    sum.bias_parts = sa.token_blocks;
+    sum.dbias = a.dbias;
+    rb::router_sum_kernel<<<sum.dw_blocks + (a.dbias ? (s->E + 31) / 32 : 0), 256, 0, st>>>(sum);
     return launch_status();
 }
 
@@ -1814,8 +1978,7 @@ moe_route_backward_workspace_size(const moe_shape_t *shape)
 {
     if (check_shape(shape, false, nullptr) != MOE_OK)
         return 0;
-    const size_t n = route_backward_scratch(shape);
-    return n ? n : kAlign;
+    return route_back_layout(shape).total;
 }
 
 __attribute__((visibility("default"))) moe_status_t
@@ -1849,7 +2012,7 @@ moe_route_backward(const moe_shape_t *shape, const uint16_t *x, const float *w_r
         (dtopk_w && !aligned4(dtopk_w)) || (dlogits && !aligned16(dlogits)) ||
         (dx_add && !aligned16(dx_add)) || (dx && !aligned16(dx)))
         return MOE_ERR_MISALIGNED;
-    if (!ws || ws_bytes < route_backward_scratch(shape))
+    if (!ws || ws_bytes < route_back_layout(shape).total)
         return MOE_ERR_WORKSPACE_TOO_SMALL;
     if (!aligned16(ws))
         return MOE_ERR_MISALIGNED;
