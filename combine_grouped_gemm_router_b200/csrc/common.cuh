@@ -191,6 +191,16 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
 }
 
 
+// Programmatic dependent launch: a kernel launched so may start while the one before it on the
+// stream still runs; grid_wait() returns when that one has completed and its writes are visible
+// (at once in a kernel launched the ordinary way). grid_go() lets the kernel after this one be
+// scheduled as soon as every block of this one has started.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_go()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // Token block b of the dispatch: blocks never straddle a home-rank shard, so
 // per-shard prefix counts are available at block boundaries.
 // shard = b / bps, tokens [shard*S + (b%bps)*HB, min(... + HB, (shard+1)*S)).

@@ -276,6 +276,24 @@ int row_blocks(int N, int nchunks, int seg)
 }
 
 
+// Launch that may overlap the end of the kernel before it on the stream (see grid_wait).
+template <typename... P, typename... A>
+cudaError_t launch_chained(void (*kern)(P...), int blocks, int threads, size_t smem,
+                           cudaStream_t st, A &&...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(blocks, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
 inline moe_status_t launch_status()
 {
     return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
@@ -1233,53 +1251,59 @@ struct RouteBackLayout {
     size_t dl, wp, bias, part, total;
 };
 
-// dWr's tiles: 128 MT columns of x, 128-token chunks, split evenly over G CTAs.
+// dWr's tiles: `cols` columns of x by `rows` experts (padded); each tile's 128-token chunks in
+// `parts` equal shares, a CTA each.
 struct DwGeometry {
-    int ne, mt, tiles, chunks, G, kmax;
+    int ne, rows, cols, tiles, chunks, parts;
 };
 
 DwGeometry dw_geometry(const moe_shape_t *s)
 {
     DwGeometry g;
     g.ne = (s->E + 63) / 64;
-    // two M tiles share a stage's planes of dl (half the L2 reads of them) while TMEM holds
-    // both accumulators twice
-    g.mt = g.ne <= 2 ? 2 : 1;
-    g.tiles = (s->d + 128 * g.mt - 1) / (128 * g.mt);
+    g.rows = g.ne > 2 ? 256 : 128;
+    g.cols = g.ne > 2 ? 128 : 256;
+    g.tiles = (s->d + g.cols - 1) / g.cols;
     g.chunks = (s->N + rb::kChunk - 1) / rb::kChunk;
-    const int64_t U = (int64_t)g.tiles * g.chunks;
-    g.G = (int)(U < num_sms() ? U : num_sms());
-    g.kmax = g.G > 0 ? (int)((g.chunks + U / g.G - 1) / (U / g.G)) + 1 : 1;
+    g.parts = num_sms() / g.tiles;
+    if (g.parts > g.chunks)
+        g.parts = g.chunks;
+    if (g.parts < 1)
+        g.parts = 1;
     return g;
 }
 
 int split_blocks(const moe_shape_t *s)
 {
-    const int64_t want = ((int64_t)s->N + 15) / 16;
+    const int64_t want = ((int64_t)s->N + 31) / 32;
     const int64_t most = 4 * (int64_t)num_sms();
     return (int)(want < most ? want : most);
 }
 
+// Columns of a row of dl's planes: whole boxes of 64 experts, or (one box, whose copies end at E)
+// a multiple of 16 bytes.
+int dl_pitch_of(const moe_shape_t *s) { return s->E > 64 ? (s->E + 63) & ~63 : (s->E + 7) & ~7; }
+
 RouteBackLayout route_back_layout(const moe_shape_t *s)
 {
     RouteBackLayout L;
-    const size_t pitch = ((size_t)s->E + 7) & ~(size_t)7;
+    const size_t pitch = dl_pitch_of(s);
     const DwGeometry g = dw_geometry(s);
     size_t o = 0;
     L.dl = o;
     o = align_up(o + 3 * (size_t)s->N * pitch * 2);
     L.wp = o;
-    o = align_up(o + 3 * (size_t)s->E * s->d * 2);
+    o = align_up(o + 3 * (size_t)s->E * ((s->d + 63) / 64 * 64) * 2);
     L.bias = o;
     o = align_up(o + (size_t)split_blocks(s) * s->E * 4);
     L.part = o;
-    o = align_up(o + (size_t)g.tiles * g.kmax * s->E * 128 * g.mt * 4);
+    o = align_up(o + (size_t)g.tiles * g.parts * g.rows * g.cols * 4);
     L.total = o;
     return L;
 }
 
-// Tensor map of `rank` (2 or 3) dimensions, innermost first; pitch: bytes of a row and (3-D)
-// of a plane. Elements outside the extents read as zeros and are not written.
+// Tensor map of `rank` (2 to 4) dimensions, innermost first; pitch: bytes between the indexes of
+// the dimensions after it. Elements outside the extents read as zeros and are not written.
 bool make_tmap_box(CUtensorMap *m, CUtensorMapDataType dt, int rank, const void *ptr,
                    const cuuint64_t *dims, const cuuint64_t *pitch, const cuuint32_t *box,
                    CUtensorMapSwizzle swizzle)
@@ -1287,63 +1311,68 @@ bool make_tmap_box(CUtensorMap *m, CUtensorMapDataType dt, int rank, const void 
     auto enc = tensor_map_encoder();
     if (!enc)
         return false;
-    const cuuint32_t estr[3] = {1, 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
     return enc(m, dt, rank, const_cast<void *>(ptr), dims, pitch, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <bool BF16, bool STREAM, bool ADD>
 moe_status_t launch_router_dx(const moe_shape_t *s, const uint16_t *dl, const uint16_t *wp,
                               const uint16_t *add, void *dx, cudaStream_t st)
 {
-    const bool bf16 = (s->flags & MOE_FLAG_OUT_BF16) != 0;
+    using T = rb::DxTile<BF16, STREAM, ADD>;
     const cuuint64_t N = (cuuint64_t)s->N, d = (cuuint64_t)s->d, E = (cuuint64_t)s->E;
-    const cuuint64_t pitch = (E + 7) & ~(cuuint64_t)7;
+    const cuuint64_t pitch = (cuuint64_t)dl_pitch_of(s);
     CUtensorMap t_dl, t_w, t_dx, t_add;
     const cuuint64_t dl_dims[3] = {E, N, 3}, dl_pitch[2] = {pitch * 2, N * pitch * 2};
-    const cuuint64_t w_dims[3] = {d, E, 3}, w_pitch[2] = {d * 2, E * d * 2};
-    const cuuint64_t x_dims[2] = {d, N}, dx_pitch[1] = {d * (bf16 ? 2 : 4)}, add_pitch[1] = {d * 2};
-    const cuuint32_t dl_box[3] = {64, 128, 1}, w_box[3] = {64, 64, 1};
-    const cuuint32_t p_box[2] = {(cuuint32_t)(bf16 ? 64 : 32), 32};
+    const cuuint64_t wb = (d + 63) / 64;  // boxes of columns
+    const cuuint64_t w_dims[4] = {64, E, wb, 3}, w_pitch[3] = {128, E * 128, wb * E * 128};
+    const cuuint64_t x_dims[2] = {d, N}, dx_pitch[1] = {d * (BF16 ? 2 : 4)}, add_pitch[1] = {d * 2};
+    const int nb = (s->d + 63) / 64 < T::NB ? (s->d + 63) / 64 : T::NB;
+    const cuuint32_t dl_box[3] = {STREAM ? 32 : 64, 128, STREAM ? T::PLANES : 1};
+    const cuuint32_t w_box[4] = {64, STREAM ? 32 : 64, (cuuint32_t)nb, T::PLANES};
+    const cuuint32_t p_box[2] = {(cuuint32_t)T::CP, 32};
     const CUtensorMapDataType b16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    if (!make_tmap_box(&t_dl, b16, 3, dl, dl_dims, dl_pitch, dl_box, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_tmap_box(&t_w, b16, 3, wp, w_dims, w_pitch, w_box, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_tmap_box(&t_dx, bf16 ? b16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, dx, x_dims,
-                       dx_pitch, p_box, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_tmap_box(&t_add, b16, 2, add ? add : dl, add ? x_dims : dl_dims,
-                       add ? add_pitch : dl_pitch, p_box,
-                       bf16 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+    const CUtensorMapSwizzle sw128 = CU_TENSOR_MAP_SWIZZLE_128B, sw64 = CU_TENSOR_MAP_SWIZZLE_64B;
+    if (!make_tmap_box(&t_dl, b16, 3, dl, dl_dims, dl_pitch, dl_box, STREAM ? sw64 : sw128) ||
+        !make_tmap_box(&t_w, b16, 4, wp, w_dims, w_pitch, w_box, sw128) ||
+        !make_tmap_box(&t_dx, BF16 ? b16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, dx, x_dims,
+                       dx_pitch, p_box, sw128) ||
+        (ADD && !make_tmap_box(&t_add, b16, 2, add, x_dims, add_pitch, p_box,
+                               BF16 ? sw128 : sw64)))
         return MOE_ERR_CUDA;
+    if (!ADD)
+        t_add = t_dx;  // not read
     rb::DxArgs a = {};
     a.N = s->N;
     a.d = s->d;
     a.E = s->E;
-    a.chunks = (s->E + 63) / 64;
-    const int planes = bf16 ? 2 : 3;
-    a.bn = 256;
-    while (a.bn > 64 && (planes * a.chunks * (a.bn / 64) * rb::kBox > rb::kDxMaxB ||
-                         a.bn / 2 >= s->d))
-        a.bn /= 2;
-    a.slices = (s->d + a.bn - 1) / a.bn;
+    a.nb = nb;
+    a.slices = (s->d + 64 * a.nb - 1) / (64 * a.nb);
     a.tiles = (s->N + 127) / 128;
-    const int fixed = planes * a.chunks * (a.bn / 64) * rb::kBox + rb::dx_piece_area(bf16) + 1024 +
-                      512;
-    a.units = (rb::kDxMaxSmem - fixed) / rb::kUnit;
+    const int fixed = T::weights(a.nb) + T::SLOT_AREA + 1024 + 512;
+    a.units = (rb::kDxMaxSmem - fixed) / T::unit(a.nb);
     if (a.units > rb::kDxMaxUnits)
         a.units = rb::kDxMaxUnits;
-    if (a.units < rb::kDxUnits)
-        return MOE_ERR_UNSUPPORTED_SHAPE;
-    a.add = add != nullptr;
     a.timeout_ns = kWaitTimeoutNs;
-    const int64_t U = (int64_t)a.slices * a.tiles;
-    const int G = (int)(U < num_sms() ? U : num_sms());
-    auto go = [&](auto kern) {
-        if (smem_attr_once(kern, rb::kDxMaxSmem) != cudaSuccess)
-            return MOE_ERR_CUDA;
-        kern<<<G, rb::kDxThreads, fixed + a.units * rb::kUnit, st>>>(t_dl, t_w, t_dx, t_add, a);
-        return launch_status();
-    };
-    return bf16 ? go(rb::router_dx_kernel<true>) : go(rb::router_dx_kernel<false>);
+    int blocks;
+    if (STREAM) {
+        const int64_t items = (int64_t)a.slices * a.tiles;
+        blocks = (int)(items < num_sms() ? items : num_sms());
+    } else {
+        int groups = num_sms() / a.slices;
+        if (groups > a.tiles)
+            groups = a.tiles;
+        blocks = (groups < 1 ? 1 : groups) * a.slices;
+    }
+    if (smem_attr_once(rb::router_dx_kernel<BF16, STREAM, ADD>, rb::kDxMaxSmem) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    if (launch_chained(rb::router_dx_kernel<BF16, STREAM, ADD>, blocks, T::THREADS,
+                       fixed + a.units * T::unit(a.nb), st, t_dl, t_w, t_dx, t_add, a) !=
+        cudaSuccess)
+        return MOE_ERR_CUDA;
+    return launch_status();
 }
 
 moe_status_t launch_router_dw(const moe_shape_t *s, const DwGeometry &g, const uint16_t *x,
@@ -1351,41 +1380,63 @@ moe_status_t launch_router_dw(const moe_shape_t *s, const DwGeometry &g, const u
                               cudaStream_t st)
 {
     const cuuint64_t N = (cuuint64_t)s->N, d = (cuuint64_t)s->d, E = (cuuint64_t)s->E;
-    const cuuint64_t pitch = (E + 7) & ~(cuuint64_t)7;
-    CUtensorMap t_x, t_dl;
-    const cuuint64_t x_dims[2] = {d, N}, x_pitch[1] = {d * 2};
-    const cuuint64_t dl_dims[3] = {E, N, 3}, dl_pitch[2] = {pitch * 2, N * pitch * 2};
-    const cuuint32_t x_box[2] = {64, 64}, dl_box[3] = {64, 64, 1};
+    const cuuint64_t pitch = (cuuint64_t)dl_pitch_of(s);
+    const bool x_boxes = s->d % 64 == 0;
     const CUtensorMapDataType b16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    if (!make_tmap_box(&t_x, b16, 2, x, x_dims, x_pitch, x_box, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_tmap_box(&t_dl, b16, 3, dl, dl_dims, dl_pitch, dl_box, CU_TENSOR_MAP_SWIZZLE_128B))
-        return MOE_ERR_CUDA;
-    const rb::DwArgs a{s->N, s->d, s->E, g.tiles, g.chunks, g.kmax, mask, part, kWaitTimeoutNs};
-    auto go = [&](auto kern, int smem) {
-        if (smem_attr_once(kern, smem) != cudaSuccess)
+    const CUtensorMapSwizzle sw128 = CU_TENSOR_MAP_SWIZZLE_128B;
+    const cuuint64_t dl_dims[4] = {E < 64 ? E : 64, N, (E + 63) / 64, 3};
+    const cuuint64_t dl_pitch[3] = {pitch * 2, 128, N * pitch * 2};
+    const cuuint64_t x_dims[2] = {d, N}, x_pitch[1] = {d * 2};
+    const cuuint64_t xb_dims[3] = {64, N, d / 64}, xb_pitch[2] = {d * 2, 128};
+    const rb::DwArgs a{s->N, s->d, s->E, g.tiles, g.chunks, g.parts, x_boxes, mask, part,
+                       kWaitTimeoutNs};
+    auto go = [&](auto ne) {
+        using T = rb::DwTile<decltype(ne)::value>;
+        auto kern = rb::router_dw_kernel<decltype(ne)::value>;
+        const cuuint32_t x_box[3] = {64, T::TOK, T::XB}, dl_box[4] = {64, T::TOK, decltype(ne)::value, 3};
+        CUtensorMap t_x, t_dl;
+        if (!make_tmap_box(&t_x, b16, x_boxes ? 3 : 2, x, x_boxes ? xb_dims : x_dims,
+                           x_boxes ? xb_pitch : x_pitch, x_box, sw128) ||
+            !make_tmap_box(&t_dl, b16, 4, dl, dl_dims, dl_pitch, dl_box, sw128) ||
+            smem_attr_once(kern, T::SMEM) != cudaSuccess ||
+            launch_chained(kern, g.tiles * g.parts, rb::kDwThreads, T::SMEM, st, t_x, t_dl, a) !=
+                cudaSuccess)
             return MOE_ERR_CUDA;
-        kern<<<g.G, rb::kDwThreads, smem, st>>>(t_x, t_dl, a);
         return launch_status();
     };
     switch (g.ne) {
-    case 1: return go(rb::router_dw_kernel<1, 2>, rb::DwTile<1, 2>::SMEM);
-    case 2: return go(rb::router_dw_kernel<2, 2>, rb::DwTile<2, 2>::SMEM);
-    case 3: return go(rb::router_dw_kernel<3, 1>, rb::DwTile<3, 1>::SMEM);
-    default: return go(rb::router_dw_kernel<4, 1>, rb::DwTile<4, 1>::SMEM);
+    case 1: return go(std::integral_constant<int, 1>{});
+    case 2: return go(std::integral_constant<int, 2>{});
+    case 3: return go(std::integral_constant<int, 3>{});
+    default: return go(std::integral_constant<int, 4>{});
     }
 }
 
 moe_status_t route_backward_impl(const moe_shape_t *s, const RouteBackward &a, char *ws,
                                  cudaStream_t st)
 {
+    const rb::GradIn in{a.topk_idx, a.topk_w, a.dtopk_w, a.dlogits, a.mask};
+    if (s->N <= rb::kSmallTokens && (int64_t)s->N * s->E <= rb::kSmallLogits) {
+        const rb::SmallArgs sm{in, a.x, a.w_router, a.dx_add, a.dx, a.dw, a.dbias, s->N, s->E, s->K,
+                               s->d, (s->flags & MOE_FLAG_OUT_BF16) ? 1 : 0};
+        const int blocks = (s->d + rb::kSmallCols - 1) / rb::kSmallCols;
+        moe_status_t rc = MOE_OK;
+        row_slices(s->E, [&](auto lpr, auto) {
+            auto kern = rb::router_small_grad_kernel<decltype(lpr)::value>;
+            if (smem_attr_once(kern, rb::kSmallSmem) != cudaSuccess)
+                rc = MOE_ERR_CUDA;
+            else
+                kern<<<blocks, 256, rb::small_smem(s->N, s->E), st>>>(sm);
+        });
+        return rc != MOE_OK ? rc : launch_status();
+    }
     const RouteBackLayout L = route_back_layout(s);
     const DwGeometry g = dw_geometry(s);
     uint16_t *dl = reinterpret_cast<uint16_t *>(ws + L.dl);
     uint16_t *wp = reinterpret_cast<uint16_t *>(ws + L.wp);
     float *bias = reinterpret_cast<float *>(ws + L.bias);
     float *part = reinterpret_cast<float *>(ws + L.part);
-    rb::SplitArgs sa{a.topk_idx, a.topk_w, a.dtopk_w, a.dlogits, a.mask, a.dx ? a.w_router : nullptr,
-                     s->N, s->E, s->K, s->d, (s->E + 7) & ~7, dl, wp, bias, split_blocks(s)};
+    rb::SplitArgs sa{in, a.dx ? a.w_router : nullptr, s->N, s->E, s->K, s->d, dl_pitch_of(s), dl, wp, bias, split_blocks(s)};
     int w_blocks = 0;
     if (a.dx) {
         const int64_t want = ((int64_t)s->E * s->d / 8 + rb::kSplitThreads - 1) / rb::kSplitThreads;
@@ -1396,8 +1447,17 @@ moe_status_t route_backward_impl(const moe_shape_t *s, const RouteBackward &a, c
             <<<sa.token_blocks + w_blocks, rb::kSplitThreads, 0, st>>>(sa);
     });
     moe_status_t rc = launch_status();
-    if (rc == MOE_OK && a.dx)
-        rc = launch_router_dx(s, dl, wp, a.dx_add, a.dx, st);
+    if (rc == MOE_OK && a.dx) {
+        const bool bf16 = (s->flags & MOE_FLAG_OUT_BF16) != 0;
+        auto go = [&](auto b, auto add) {
+            constexpr bool B = decltype(b)::value, A = decltype(add)::value;
+            return s->E <= 64 ? launch_router_dx<B, false, A>(s, dl, wp, a.dx_add, a.dx, st)
+                              : launch_router_dx<B, true, A>(s, dl, wp, a.dx_add, a.dx, st);
+        };
+        const std::true_type yes;
+        const std::false_type no;
+        rc = bf16 ? (a.dx_add ? go(yes, yes) : go(yes, no)) : (a.dx_add ? go(no, yes) : go(no, no));
+    }
     if (rc == MOE_OK && a.dw)
         rc = launch_router_dw(s, g, a.x, dl, a.mask, part, st);
     if (rc != MOE_OK || (!a.dw && !a.dbias))
@@ -1405,18 +1465,19 @@ moe_status_t route_backward_impl(const moe_shape_t *s, const RouteBackward &a, c
     rb::SumArgs sum = {};
     sum.d = s->d;
     sum.E = s->E;
-    sum.tile_cols = 128 * g.mt;
-    sum.tiles = g.tiles;
-    sum.chunks = g.chunks;
-    sum.kmax = g.kmax;
-    sum.G = g.G;
+    sum.tile_cols = g.cols;
+    sum.tile_rows = g.rows;
+    sum.fold = g.ne == 1;
+    sum.parts = g.parts;
     sum.part = part;
     sum.dw = a.dw;
     sum.dw_blocks = a.dw ? (int)(((int64_t)s->E * s->d / 4 + 255) / 256) : 0;
     sum.bias_part = bias;
     sum.bias_parts = sa.token_blocks;
     sum.dbias = a.dbias;
-    rb::router_sum_kernel<<<sum.dw_blocks + (a.dbias ? (s->E + 31) / 32 : 0), 256, 0, st>>>(sum);
+    if (launch_chained(rb::router_sum_kernel, sum.dw_blocks + (a.dbias ? (s->E + 7) / 8 : 0), 256,
+                       0, st, sum) != cudaSuccess)
+        return MOE_ERR_CUDA;
     return launch_status();
 }
 

@@ -14,10 +14,12 @@
 //   dx, fp32: hi hi + hi mid + mid hi + mid mid + hi lo + lo hi (what is left out is below
 //       2^-23 of the product); bf16: hi hi + hi mid + mid hi (below 2^-14, against the output's
 //       own rounding of 2^-8).
-// Four launches: the split (router_split_grad_kernel), dx, dWr, and the sum of dWr's and dbias's
-// partial results in a fixed order. No atomics: the same bits every run.
+// Four launches (one for a few tokens, router_small_grad_kernel): the split (router_split_grad_kernel), dx, dWr, and the sum of dWr's and dbias's
+// partial results in a fixed order, each scheduled while the one before it drains (grid_wait).
+// No atomics: the same bits every run.
 #pragma once
 
+#include "balance.cuh"
 #include "common.cuh"
 #include "grouped_gemm.cuh"
 
@@ -26,54 +28,171 @@ namespace rb {
 
 constexpr int kBox = 8192;  // shared memory of a 64-row x 128-byte TMA box
 
-// v = p[0] + p[1] + p[2] in bf16 terms (bits). Not finite: all of it in p[0].
-__device__ __forceinline__ void split3(float v, uint32_t (&p)[3])
-{
-    uint32_t h = pack_bf16x2(v, 0.0f) & 0xFFFFu;
-    if (!isfinite(__uint_as_float(h << 16))) {
-        if (!isfinite(v)) {
-            p[0] = h;
-            p[1] = p[2] = 0;
-            return;
-        }
-        h = __float_as_uint(v) >> 16;  // rounds past the largest bf16: truncated instead
-    }
-    const float r = v - __uint_as_float(h << 16);
-    const uint32_t m = pack_bf16x2(r, 0.0f) & 0xFFFFu;
-    p[0] = h;
-    p[1] = m;
-    p[2] = pack_bf16x2(r - __uint_as_float(m << 16), 0.0f) & 0xFFFFu;
-}
-
-// Eight values -> 16 bytes of each of the three planes.
+// Eight values -> 16 bytes of each of the three planes: v = out[0] + out[1] + out[2].
 __device__ __forceinline__ void split3x8(const float (&v)[8], uint4 (&out)[3])
 {
-    uint32_t w[3][4];
+    uint32_t w[3][4], top = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        uint32_t a[3], b[3];
-        split3(v[2 * i], a);
-        split3(v[2 * i + 1], b);
+        const float a = v[2 * i], b = v[2 * i + 1];
+        w[0][i] = pack_bf16x2(a, b);
+        const float ra = a - bf16_lo(w[0][i]), rb = b - bf16_hi(w[0][i]);
+        w[1][i] = pack_bf16x2(ra, rb);
+        w[2][i] = pack_bf16x2(ra - bf16_lo(w[1][i]), rb - bf16_hi(w[1][i]));
+        top = max(top, max(__float_as_uint(a) & 0x7FFFFFFFu, __float_as_uint(b) & 0x7FFFFFFFu));
+    }
+    if (top >= 0x7F7F8000u) {
+        // infinite, NaN, or a value that rounds past the largest bf16: the first term is the
+        // value truncated (a NaN stays one), the others what is left of a finite value
 #pragma unroll
-        for (int p = 0; p < 3; ++p)
-            w[p][i] = a[p] | (b[p] << 16);
+        for (int j = 0; j < 8; ++j) {
+            uint32_t h = __float_as_uint(v[j]) >> 16, m = 0, l = 0;
+            if (isnan(v[j]))
+                h |= 0x40u;
+            else if (!isinf(v[j])) {
+                const float r = v[j] - __uint_as_float(h << 16);
+                m = pack_bf16x2(r, 0.0f) & 0xFFFFu;
+                l = pack_bf16x2(r - __uint_as_float(m << 16), 0.0f) & 0xFFFFu;
+            }
+            const uint32_t t[3] = {h, m, l};
+#pragma unroll
+            for (int p = 0; p < 3; ++p)
+                w[p][j / 2] = (j & 1) ? (w[p][j / 2] & 0xFFFFu) | (t[p] << 16)
+                                      : (w[p][j / 2] & 0xFFFF0000u) | t[p];
+        }
     }
 #pragma unroll
     for (int p = 0; p < 3; ++p)
         out[p] = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
 }
 
-struct SplitArgs {
+// What the gradient of the logits is made of.
+struct GradIn {
     const int32_t *topk_idx;
     const float *topk_w, *dtopk_w;  // dtopk_w nullable
     const float *dlogits;           // nullable
     const uint8_t *mask;            // nullable
-    const float *wr;                // nullable: no planes of the router weights wanted
+};
+
+// dl of token t in the 8 neighbouring columns from 8 l, LPR lanes to a token (all lanes of the
+// warp call). Zeros for a masked token (whatever its inputs hold) and past the last one. row:
+// the lane group's 8 LPR floats of shared memory, where the slots' gradients meet their columns.
+template <int LPR>
+__device__ __forceinline__ void token_dlogits(const GradIn &in, int N, int E, int K, int64_t t,
+                                              int l, float *row, float (&v)[8])
+{
+    const int c0 = 8 * l;
+    const bool inside = t < N;
+    // a masked token's inputs are read all the same (and dropped): no load waits for the mask
+    const bool live = inside && (!in.mask || in.mask[t]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        v[j] = 0.0f;
+    if (inside && in.dlogits) {
+        const float *src = in.dlogits + t * E;
+        if (E % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (c0 + 4 * i < E) {
+                    const float4 q = *reinterpret_cast<const float4 *>(src + c0 + 4 * i);
+                    v[4 * i] = q.x;
+                    v[4 * i + 1] = q.y;
+                    v[4 * i + 2] = q.z;
+                    v[4 * i + 3] = q.w;
+                }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c0 + j < E)
+                    v[j] = src[c0 + j];
+        }
+    }
+    if (!live) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = 0.0f;
+    }
+    if (!in.dtopk_w)
+        return;
+    // slot k of the token, or zeros
+    auto slot = [&](int k, int &idx, float &w, float &dw) {
+        idx = -1;
+        w = dw = 0.0f;
+        if (k < K && inside) {
+            idx = in.topk_idx[t * K + k];
+            w = in.topk_w[t * K + k];
+            dw = in.dtopk_w[t * K + k];
+            if (!live || (unsigned)idx >= (unsigned)E) {
+                if (live)
+                    set_dev_error(MOE_ERR_DEVICE_BOUNDS);
+                idx = -1;
+                w = dw = 0.0f;
+            }
+        }
+    };
+    // lane l takes the slots l, l + LPR, ...
+    float s = 0.0f;
+    int idx, idx0 = -1;
+    float w, dw, w0 = 0.0f, dw0 = 0.0f;
+    for (int k0 = 0; k0 < K; k0 += LPR) {
+        slot(k0 + l, idx, w, dw);
+        if (k0 == 0) {
+            idx0 = idx;
+            w0 = w;
+            dw0 = dw;
+        }
+        s += w * dw;
+    }
+    s = row_sum<LPR>(s);
+    *reinterpret_cast<float4 *>(row + c0) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4 *>(row + c0 + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    __syncwarp();
+    for (int k0 = 0; k0 < K; k0 += LPR) {
+        if (k0 == 0) {
+            idx = idx0;
+            w = w0;
+            dw = dw0;
+        } else {
+            slot(k0 + l, idx, w, dw);
+        }
+        const float g = w * (dw - s);
+        // an expert twice among these slots (no router's top-K, but allowed): one after another
+        const uint32_t same = __match_any_sync(0xffffffffu, idx < 0 ? -1 - (int)(threadIdx.x & 31)
+                                                                    : idx + (((threadIdx.x & 31) / LPR) << 16));
+        const bool lone = (same & (same - 1)) == 0;
+        if (__all_sync(0xffffffffu, lone)) {
+            if (idx >= 0)
+                row[idx] += g;
+            __syncwarp();
+        } else {
+            for (int o = 0; o < LPR; ++o) {
+                if (l == o && idx >= 0)
+                    row[idx] += g;
+                __syncwarp();
+            }
+        }
+    }
+    const float4 a = *reinterpret_cast<const float4 *>(row + c0);
+    const float4 b = *reinterpret_cast<const float4 *>(row + c0 + 4);
+    v[0] = a.x;
+    v[1] = a.y;
+    v[2] = a.z;
+    v[3] = a.w;
+    v[4] = b.x;
+    v[5] = b.y;
+    v[6] = b.z;
+    v[7] = b.w;
+    __syncwarp();
+}
+
+struct SplitArgs {
+    GradIn in;
+    const float *wr;  // nullable: no planes of the router weights wanted
     int N, E, K, d;
-    int pitch;        // E rounded up to 8: columns of a row of the planes
+    int pitch;        // columns of a row of dl's planes, the ones past E zeros
     uint16_t *dl;     // [3][N][pitch]
-    uint16_t *wp;     // [3][E][d]
-    float *bias_part; // [token_blocks][E]
+    uint16_t *wp;     // [3][d / 64 rounded up][E][64]: a box of 64 columns of x in one piece
+    float *bias_part; // [E][token_blocks]
     int token_blocks;
 };
 
@@ -87,6 +206,7 @@ __global__ void __launch_bounds__(kSplitThreads) router_split_grad_kernel(const 
 {
     constexpr int GW = 32 / LPR, WARPS = kSplitThreads / 32;
     const int tid = threadIdx.x;
+    grid_go();
     if ((int)blockIdx.x >= a.token_blocks) {
         const int64_t n = (int64_t)a.E * a.d / 8;  // d % 8 == 0
         const int64_t step = (int64_t)(gridDim.x - a.token_blocks) * kSplitThreads;
@@ -97,64 +217,30 @@ __global__ void __launch_bounds__(kSplitThreads) router_split_grad_kernel(const 
             const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
             uint4 out[3];
             split3x8(v, out);
+            const int e = (int)(i / (a.d / 8)), c = (int)(i - (int64_t)e * (a.d / 8));  // 8 columns
+            const int blocks = (a.d + 63) / 64;
 #pragma unroll
             for (int p = 0; p < 3; ++p)
-                reinterpret_cast<uint4 *>(a.wp)[p * n + i] = out[p];
+                reinterpret_cast<uint4 *>(a.wp)[(((size_t)p * blocks + c / 8) * a.E + e) * 8 +
+                                                (c & 7)] = out[p];
         }
         return;
     }
     __shared__ float s_sum[WARPS * LPR * 8];
+    __shared__ __align__(16) float s_row[WARPS * 256];
     const int warp = tid >> 5, lane = tid & 31, l = lane % LPR, grp = lane / LPR;
-    const int c0 = 8 * l, E = a.E, K = a.K;
+    const int c0 = 8 * l, E = a.E;
     const size_t plane = (size_t)a.N * a.pitch;
     float sum[8] = {};
     const int64_t stride = (int64_t)a.token_blocks * WARPS * GW;
-    for (int64_t t = ((int64_t)blockIdx.x * WARPS + warp) * GW + grp; t < a.N; t += stride) {
-        const bool live = !a.mask || a.mask[t];
-        float v[8] = {};
-        if (live && a.dlogits) {
-            const float *row = a.dlogits + t * E;
-            if (E % 4 == 0) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if (c0 + 4 * i < E) {
-                        const float4 q = *reinterpret_cast<const float4 *>(row + c0 + 4 * i);
-                        v[4 * i] = q.x;
-                        v[4 * i + 1] = q.y;
-                        v[4 * i + 2] = q.z;
-                        v[4 * i + 3] = q.w;
-                    }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (c0 + j < E)
-                        v[j] = row[c0 + j];
-            }
-        }
-        if (live && a.dtopk_w) {
-            const int32_t *idx = a.topk_idx + t * K;
-            const float *w = a.topk_w + t * K, *dw = a.dtopk_w + t * K;
-            float s = 0.0f;
-            for (int k = 0; k < K; ++k) {
-                if ((unsigned)idx[k] < (unsigned)E)
-                    s += w[k] * dw[k];
-                else if (l == 0)
-                    set_dev_error(MOE_ERR_DEVICE_BOUNDS);
-            }
-            for (int k = 0; k < K; ++k) {
-                const int c = idx[k] - c0;
-                if ((unsigned)idx[k] < (unsigned)E && (unsigned)c < 8u) {
-                    const float g = w[k] * (dw[k] - s);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        v[j] += j == c ? g : 0.0f;
-                }
-            }
-        }
+    for (int64_t t0 = ((int64_t)blockIdx.x * WARPS + warp) * GW; t0 < a.N; t0 += stride) {
+        const int64_t t = t0 + grp;
+        float v[8];
+        token_dlogits<LPR>(a.in, a.N, E, a.K, t, l, s_row + warp * 256 + grp * (8 * LPR), v);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             sum[j] += v[j];
-        if (c0 < a.pitch) {
+        if (t < a.N && c0 < a.pitch) {
             uint4 out[3];
             split3x8(v, out);
 #pragma unroll
@@ -180,7 +266,7 @@ __global__ void __launch_bounds__(kSplitThreads) router_split_grad_kernel(const 
 #pragma unroll
         for (int w = 0; w < WARPS; ++w)
             s += s_sum[w * (LPR * 8) + tid];
-        a.bias_part[(size_t)blockIdx.x * E + tid] = s;
+        a.bias_part[(size_t)tid * a.token_blocks + blockIdx.x] = s;
     }
 }
 
@@ -193,6 +279,16 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y,
+                                            int z, int w, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
         : "memory");
 }
 
@@ -211,62 +307,76 @@ __host__ __device__ constexpr uint32_t idesc(int M, int N, bool a_mn, bool b_mn)
     return gg::instr_desc_bf16(M, N) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16);
 }
 
-struct Span {  // work items [u0, u1) of CTA c of G: an even, contiguous share of U
-    int64_t u0, u1;
-    __host__ __device__ Span(int64_t U, int G, int c) : u0(U * c / G), u1(U * (c + 1) / G) {}
-};
-// The CTA whose span holds item v.
-__host__ __device__ inline int span_owner(int64_t U, int G, int64_t v)
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
 {
-    return (int)(((v + 1) * G - 1) / U);
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(r));
+    return r != 0;
 }
 
 // ---------------------------------------------------------------- dWr = dl^T x
 
-// D[d'][e] over a chunk of kChunk tokens: M = d' (MT tiles of 128 columns of x), N = e, K =
+// D[e][d'] over a chunk of kChunk tokens: M = e (128 rows), N = d' (64 XB columns of x), K =
 // tokens. Both operands lie in memory with the token as the slow index, so both are the
-// M/N-contiguous kind. A chunk's sum is read back and added to fp32 registers before it is
-// longer than 128 tokens: the tensor core's accumulator truncates, and a truncation per step
-// over tens of thousands of tokens would cost the low bits that the split keeps.
-constexpr int kTok = 64;     // tokens of a shared-memory stage
-constexpr int kChunk = 128;  // tokens of a work item (accumulated in TMEM)
+// M/N-contiguous kind. e is M and d' is N because an M = 128 MMA costs 64 cycles however small
+// N is (measured: 70 at N = 64 and 128, 130 at 256: its A operand is read at 64 bytes a
+// cycle), so the wide side has to be N. Up to 64 experts, one M tile holds two planes (rows
+// e: hi and lo, rows 64 + e: mid), which router_sum_kernel adds; the fourth quarter of A is a box of
+// zeros. A chunk's sum is read back and added to fp32 registers before it is longer than 128
+// tokens: the tensor core's accumulator truncates, and a truncation per step over tens of
+// thousands of tokens would cost the low bits that the split keeps.
+// The CTAs of one share of the tokens walk over them together, one column tile each, so that
+// rows of x are read whole within a short time.
+constexpr int kChunk = 128;  // tokens accumulated in TMEM
 constexpr int kDwThreads = 384;
 
-template <int NE, int MT>
+template <int NE>  // E rounded up to 64 NE
 struct DwTile {
-    static constexpr int STAGE = (2 * MT + 3 * NE) * kBox;
-    static constexpr int STAGES = 231168 / STAGE > 4 ? 4 : 231168 / STAGE;  // within 227 KB
-    static constexpr int SMEM = STAGES * STAGE + 1024 + 256;
-    static constexpr int REGS = MT == 2 ? 64 * NE : 32 * NE;  // columns of one epilogue thread
-    static_assert(STAGES >= 2 && 2 * MT * 64 * NE <= 512, "tile");
+    // tokens of a shared-memory stage. 64; 32 where two stages of 64 are all that fits (NE = 2:
+    // 57 -> 48 us at 16384 x 4096 x 128), though not where the zeroing of masked rows is what a
+    // stage waits for (NE = 1: 64 against 80 us with a mask at 32768 x 4096 x 64)
+    static constexpr int TOK = NE == 2 ? 32 : 64;
+    static constexpr int BOX = TOK * 128;       // a box of them: 64 columns
+    static constexpr int MT = NE > 2 ? 2 : 1;   // M tiles
+    static constexpr int XB = NE > 2 ? 2 : 4;   // boxes of 64 columns of x
+    static constexpr int STAGE = (XB + 3 * NE) * BOX;
+    static constexpr int ZERO = NE % 2 ? BOX : 0;
+    static constexpr int FIT = (231168 - ZERO) / STAGE;  // within 227 KB
+    static constexpr int STAGES = FIT > 8 ? 8 : FIT;
+    static constexpr int SMEM = STAGES * STAGE + ZERO + 1024 + 256;
+    static_assert(STAGES >= 2, "tile");
 };
 
 struct DwArgs {
     int N, d, E;
-    int tiles;       // column tiles of 128 MT
+    int tiles;       // column tiles of 64 XB
     int chunks;      // chunks of kChunk tokens
-    int kmax;        // partial results kept per tile, at most
+    int parts;       // equal shares of the chunks, one CTA each for every tile
+    int x_boxes;     // tm_x is [d / 64][N][64] (d % 64 == 0), else [N][d]
     const uint8_t *mask;
-    float *part;     // [tiles][kmax][E][128 MT]
+    float *part;     // [tiles][parts][128 MT][64 XB]
     uint64_t timeout_ns;
 };
 
 // Warps: 0 TMA, 1 MMA, 2 zeroes the rows of x of masked tokens (a masked row may hold NaN, and
 // 0 * NaN would reach every sum), 4..11 the running sums.
-template <int NE, int MT>
+template <int NE>
 __global__ void __launch_bounds__(kDwThreads, 1)
     router_dw_kernel(const __grid_constant__ CUtensorMap tm_x,
                      const __grid_constant__ CUtensorMap tm_dl, const DwArgs a)
 {
-    using T = DwTile<NE, MT>;
-    constexpr int S = T::STAGES;
+    using T = DwTile<NE>;
+    constexpr int S = T::STAGES, MT = T::MT, XB = T::XB, TOK = T::TOK, BOX = T::BOX;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S * T::STAGE);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S * T::STAGE + T::ZERO);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 3 * S + 5);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    const uint32_t base = smem_u32(smem), bar0 = smem_u32(bars);
+    const uint32_t base = smem_u32(smem), zero = base + S * T::STAGE, bar0 = smem_u32(bars);
     auto full = [&](int s) { return bar0 + 8u * s; };
     auto clean = [&](int s) { return bar0 + 8u * (S + s); };
     auto empty = [&](int s) { return bar0 + 8u * (2 * S + s); };
@@ -274,7 +384,9 @@ __global__ void __launch_bounds__(kDwThreads, 1)
     auto tempty = [&](int i) { return bar0 + 8u * (3 * S + 2 + i); };
     const uint32_t done = bar0 + 8u * (3 * S + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const Span span((int64_t)a.tiles * a.chunks, gridDim.x, blockIdx.x);
+    const int tile = blockIdx.x % a.tiles, part = blockIdx.x / a.tiles;
+    const int c0 = (int)((int64_t)a.chunks * part / a.parts);
+    const int c1 = (int)((int64_t)a.chunks * (part + 1) / a.parts);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -290,6 +402,11 @@ __global__ void __launch_bounds__(kDwThreads, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         *abort_flag = 0;
     }
+    if (T::ZERO) {
+        for (int i = threadIdx.x; i < T::ZERO / 16; i += kDwThreads)
+            reinterpret_cast<uint4 *>(smem + S * T::STAGE)[i] = make_uint4(0, 0, 0, 0);
+        gg::fence_proxy_async_smem();
+    }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(tmem_slot)),
@@ -297,14 +414,16 @@ __global__ void __launch_bounds__(kDwThreads, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    grid_go();
+    grid_wait();  // the planes of the kernel before
     gg::tc_fence_before();
     __syncthreads();
     gg::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    // stages of chunk c: the last one may have tokens for one stage only
-    auto stages_of = [&](int64_t c) {
-        const int64_t left = a.N - c * kChunk;
-        return left > kTok ? 2 : 1;
+    // stages of chunk c: the last one may have tokens for some only
+    auto stages_of = [&](int c) {
+        const int64_t left = a.N - (int64_t)c * kChunk;
+        return left >= kChunk ? kChunk / TOK : (int)((left + TOK - 1) / TOK);
     };
 
     if (warp == 0) {
@@ -315,26 +434,23 @@ __global__ void __launch_bounds__(kDwThreads, 1)
             for (int s = 0; s < S; ++s)
                 issued[s] = false;
             bool ok = true;
-            for (int64_t u = span.u0; u < span.u1 && ok; ++u) {
-                const int64_t tile = u / a.chunks, c = u - tile * a.chunks;
+            for (int c = c0; c < c1 && ok; ++c) {
                 for (int q = 0; q < stages_of(c); ++q) {
                     if (!gg::mbar_wait(empty(stage), phase ^ 1u, abort_flag, a.timeout_ns)) {
                         ok = false;
                         break;
                     }
                     const uint32_t dst = base + stage * T::STAGE;
-                    const int t0 = (int)(c * kChunk) + q * kTok;
+                    const int t0 = c * kChunk + q * TOK;
                     mbar_arrive_expect_tx(full(stage), T::STAGE);
-#pragma unroll
-                    for (int b = 0; b < 2 * MT; ++b)
-                        gg::tma_load_2d(dst + b * kBox, &tm_x, (int)tile * 128 * MT + 64 * b, t0,
-                                        full(stage));
-#pragma unroll
-                    for (int p = 0; p < 3; ++p)
-#pragma unroll
-                        for (int b = 0; b < NE; ++b)
-                            tma_load_3d(dst + (2 * MT + p * NE + b) * kBox, &tm_dl, 64 * b, t0, p,
-                                        full(stage));
+                    if (a.x_boxes)  // [box of columns][token][64]: all of them in one copy
+                        tma_load_3d(dst, &tm_x, 0, t0, tile * XB, full(stage));
+                    else
+                        for (int b = 0; b < XB; ++b)
+                            gg::tma_load_2d(dst + b * BOX, &tm_x, (tile * XB + b) * 64, t0,
+                                            full(stage));
+                    // [plane][box of experts][token][64]
+                    tma_load_4d(dst + XB * BOX, &tm_dl, 0, t0, 0, 0, full(stage));
                     issued[stage] = true;
                     last[stage] = phase;
                     if (++stage == S) {
@@ -348,18 +464,16 @@ __global__ void __launch_bounds__(kDwThreads, 1)
                     gg::mbar_wait(full(s), last[s], abort_flag, a.timeout_ns, false);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            const int n = (a.E + 15) & ~15;
-            const uint32_t id = idesc(128, n, true, true);
+        if (elect_one()) {
+            constexpr uint32_t id = idesc(128, 64 * XB, true, true);
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true;
-            for (int64_t u = span.u0; u < span.u1 && ok; ++u) {
-                const int64_t c = u % a.chunks;
+            for (int c = c0; c < c1 && ok; ++c) {
                 if (!gg::mbar_wait(tempty(acc), acc_phase ^ 1u, abort_flag, a.timeout_ns))
                     break;
                 gg::tc_fence_after();
-                const uint32_t d0 = tmem + (uint32_t)(acc * MT * 64 * NE);
+                const uint32_t d0 = tmem + (uint32_t)(acc * 256);
                 const int ns = stages_of(c);
                 for (int q = 0; q < ns; ++q) {
                     if (!gg::mbar_wait(a.mask ? clean(stage) : full(stage), phase, abort_flag,
@@ -368,17 +482,34 @@ __global__ void __launch_bounds__(kDwThreads, 1)
                         break;
                     }
                     gg::tc_fence_after();
-                    const uint32_t xa = base + stage * T::STAGE, pb = xa + 2 * MT * kBox;
+                    const uint32_t xa = base + stage * T::STAGE, pb = xa + XB * BOX;
+                    const uint64_t bdesc = smem_desc_mn_sw128(xa, BOX);
+                    // 16 tokens are 2048 bytes: 128 of the descriptor's address units
+                    if constexpr (NE == 1) {
+                        const uint64_t lo = smem_desc_mn_sw128(pb + 2 * BOX, zero - pb - 2 * BOX);
+                        const uint64_t him = smem_desc_mn_sw128(pb, BOX);
 #pragma unroll
-                    for (int p = 2; p >= 0; --p)  // the small terms first
+                        for (int k = 0; k < TOK / 16; ++k)  // the small terms first
+                            gg::tc_mma<0>(d0, lo + 128 * k, bdesc + 128 * k, id,
+                                          (q > 0 || k > 0) ? 1u : 0u);
 #pragma unroll
-                        for (int k = 0; k < kTok / 16; ++k)
+                        for (int k = 0; k < TOK / 16; ++k)
+                            gg::tc_mma<0>(d0, him + 128 * k, bdesc + 128 * k, id, 1u);
+                    } else {
 #pragma unroll
-                            for (int mt = 0; mt < MT; ++mt)
-                                gg::tc_mma<0>(d0 + mt * 64 * NE,
-                                              smem_desc_mn_sw128(xa + 2 * mt * kBox + k * 2048, kBox),
-                                              smem_desc_mn_sw128(pb + p * NE * kBox + k * 2048, kBox),
-                                              id, (q > 0 || p < 2 || k > 0) ? 1u : 0u);
+                        for (int p = 2; p >= 0; --p)
+#pragma unroll
+                            for (int mt = 0; mt < MT; ++mt) {
+                                const uint32_t at = pb + (p * NE + 2 * mt) * BOX;
+                                const uint64_t adesc =
+                                    smem_desc_mn_sw128(at, 2 * mt + 1 < NE ? BOX : zero - at);
+#pragma unroll
+                                for (int k = 0; k < TOK / 16; ++k)
+                                    gg::tc_mma<0>(d0 + mt * 64 * XB, adesc + 128 * k,
+                                                  bdesc + 128 * k, id,
+                                                  (q > 0 || p < 2 || k > 0) ? 1u : 0u);
+                            }
+                    }
                     gg::tc_commit(empty(stage));
                     if (++stage == S) {
                         stage = 0;
@@ -400,29 +531,33 @@ __global__ void __launch_bounds__(kDwThreads, 1)
             int stage = 0;
             uint32_t phase = 0;
             int ok = 1;
-            for (int64_t u = span.u0; u < span.u1 && ok; ++u) {
-                const int64_t c = u % a.chunks;
-                const int ns = stages_of(c);
-                for (int q = 0; q < ns; ++q) {
-                    const int64_t t0 = c * kChunk + q * kTok;
-                    uint32_t gone[2];
+            // the mask bytes of the next stage's tokens are loaded while this one is awaited
+            const int64_t t_end = min((int64_t)c1 * kChunk, (int64_t)a.N);
+            auto masked = [&](int64_t t0) {  // bit i: token t0 + 32 i + lane
+                uint32_t m = 0;
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int64_t t = t0 + 32 * i + lane;
-                        gone[i] = __ballot_sync(0xffffffffu, t < a.N && !a.mask[t]);
-                    }
-                    if (lane == 0)
-                        ok = gg::mbar_wait(full(stage), phase, abort_flag, a.timeout_ns) ? 1 : 0;
-                    ok = __shfl_sync(0xffffffffu, ok, 0);
-                    if (!ok)
-                        break;
+                for (int i = 0; i < TOK / 32; ++i)
+                    if (t0 + 32 * i + lane < t_end)
+                        m |= (uint32_t)(a.mask[t0 + 32 * i + lane] == 0) << i;
+                return m;
+            };
+            uint32_t next = masked((int64_t)c0 * kChunk);
+            for (int64_t t0 = (int64_t)c0 * kChunk; t0 < t_end; t0 += TOK) {
+                const uint32_t now = next;
+                next = masked(t0 + TOK);
+                if (lane == 0)
+                    ok = gg::mbar_wait(full(stage), phase, abort_flag, a.timeout_ns) ? 1 : 0;
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok)
+                    break;
+                if (__any_sync(0xffffffffu, now)) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        for (uint32_t m = gone[i]; m; m &= m - 1) {
-                            // a row of each of the 2 MT boxes: 128 bytes, 8 lanes
+                    for (int i = 0; i < TOK / 32; ++i)
+                        for (uint32_t m = __ballot_sync(0xffffffffu, now >> i & 1u); m; m &= m - 1) {
+                            // a row of each of the XB boxes: 128 bytes, 8 lanes
                             const int row = 32 * i + __ffs(m) - 1;
-                            if (lane < 16 * MT) {
-                                const uint32_t at = base + stage * T::STAGE + (lane >> 3) * kBox +
+                            if (lane < 8 * XB) {
+                                const uint32_t at = base + stage * T::STAGE + (lane >> 3) * BOX +
                                                     row * 128 + (lane & 7) * 16;
                                 asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at),
                                              "r"(0)
@@ -431,28 +566,27 @@ __global__ void __launch_bounds__(kDwThreads, 1)
                         }
                     gg::fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(clean(stage));
-                    if (++stage == S) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                }
+                if (lane == 0)
+                    mbar_arrive(clean(stage));
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1u;
                 }
             }
         }
     } else if (warp >= 4) {
-        // lane quadrant of TMEM: rows d'; the two warps of a quadrant take an M tile each
-        // (MT = 2) or half of the columns
+        // lane quadrant of TMEM: rows of D; the two warps of a quadrant take 128 of an
+        // accumulator's 256 columns each (with two M tiles: one tile each)
         const int q = warp & 3, half = (warp - 4) >> 2;
-        const int mt = MT == 2 ? half : 0, col0 = MT == 2 ? 0 : half * T::REGS;
         const uint32_t lanes = (uint32_t)(q * 32) << 16;
-        float sum[T::REGS];
+        float sum[128];
 #pragma unroll
-        for (int j = 0; j < T::REGS; ++j)
+        for (int j = 0; j < 128; ++j)
             sum[j] = 0.0f;
         int acc = 0;
         uint32_t acc_phase = 0;
-        for (int64_t u = span.u0; u < span.u1; ++u) {
+        for (int c = c0; c < c1; ++c) {
             int ok = 0;
             if (lane == 0)
                 ok = gg::mbar_wait(tfull(acc), acc_phase, abort_flag, a.timeout_ns) ? 1 : 0;
@@ -460,11 +594,9 @@ __global__ void __launch_bounds__(kDwThreads, 1)
             if (!ok)
                 break;
             gg::tc_fence_after();
-            const uint32_t ta = tmem + lanes + (uint32_t)(acc * MT * 64 * NE + mt * 64 * NE + col0);
+            const uint32_t ta = tmem + lanes + (uint32_t)(acc * 256 + half * 128);
 #pragma unroll
-            for (int j = 0; j < T::REGS; j += 16) {
-                if (col0 + j >= a.E)
-                    break;  // columns no MMA has written
+            for (int j = 0; j < 128; j += 16) {
                 uint32_t v[16];
                 gg::tmem_ld16(ta + j, v);
                 gg::tmem_ld_wait();
@@ -479,19 +611,15 @@ __global__ void __launch_bounds__(kDwThreads, 1)
             acc ^= 1;
             if (acc == 0)
                 acc_phase ^= 1u;
-            const int64_t tile = u / a.chunks;
-            if (u + 1 == span.u1 || (u + 1) / a.chunks != tile) {
-                const int k = (int)blockIdx.x - span_owner((int64_t)a.tiles * a.chunks, gridDim.x,
-                                                           tile * a.chunks);
-                float *dst = a.part + ((size_t)tile * a.kmax + k) * a.E * (128 * MT) + mt * 128 +
-                             q * 32 + lane;
+        }
+        const int row = (MT == 2 ? half * 128 : 0) + q * 32 + lane;
+        if ((NE == 1 ? (row & 63) : row) < a.E) {
+            float4 *dst = reinterpret_cast<float4 *>(
+                a.part + (((size_t)tile * a.parts + part) * (128 * MT) + row) * (64 * XB) +
+                (MT == 1 ? half * 128 : 0));
 #pragma unroll
-                for (int j = 0; j < T::REGS; ++j) {
-                    if (col0 + j < a.E)
-                        dst[(size_t)(col0 + j) * (128 * MT)] = sum[j];
-                    sum[j] = 0.0f;
-                }
-            }
+            for (int j = 0; j < 32; ++j)
+                dst[j] = make_float4(sum[4 * j], sum[4 * j + 1], sum[4 * j + 2], sum[4 * j + 3]);
         }
     }
     __syncwarp();
@@ -505,11 +633,12 @@ __global__ void __launch_bounds__(kDwThreads, 1)
 
 struct SumArgs {
     int d, E;
-    int tile_cols, tiles, chunks, kmax, G;  // dWr's partial results (part null: dWr not wanted)
+    int tile_cols, tile_rows, parts;  // dWr's partial results [tiles][parts][tile_rows][tile_cols]
+    int fold;  // rows e and e + 64 of a partial result are both expert e's
     const float *part;
     float *dw;
     int dw_blocks;
-    const float *bias_part;  // [bias_parts][E]
+    const float *bias_part;  // [E][bias_parts]
     int bias_parts;
     float *dbias;
 };
@@ -517,6 +646,7 @@ struct SumArgs {
 // dWr and dbias from their partial results, each element in the order of the tokens.
 __global__ void __launch_bounds__(256) router_sum_kernel(const SumArgs a)
 {
+    grid_wait();
     if ((int)blockIdx.x < a.dw_blocks) {
         const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // 4 columns of one expert
         const int64_t per_row = a.d / 4;
@@ -524,13 +654,14 @@ __global__ void __launch_bounds__(256) router_sum_kernel(const SumArgs a)
             return;
         const int e = (int)(i / per_row), c = 4 * (int)(i - e * per_row);
         const int tile = c / a.tile_cols;
-        const int64_t U = (int64_t)a.tiles * a.chunks, v0 = (int64_t)tile * a.chunks;
-        const int n = span_owner(U, a.G, v0 + a.chunks - 1) - span_owner(U, a.G, v0) + 1;
-        const float *p = a.part + ((size_t)tile * a.kmax * a.E + e) * a.tile_cols +
+        const float *p = a.part + ((size_t)tile * a.parts * a.tile_rows + e) * a.tile_cols +
                          (c - tile * a.tile_cols);
         float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const int step = (a.fold ? 64 : a.tile_rows) * a.tile_cols;
+        const int n = a.fold ? 2 * a.parts : a.parts;  // with fold, rows 64 apart: tile_rows = 128
+#pragma unroll 8
         for (int k = 0; k < n; ++k) {
-            const float4 q = *reinterpret_cast<const float4 *>(p + (size_t)k * a.E * a.tile_cols);
+            const float4 q = *reinterpret_cast<const float4 *>(p + (size_t)k * step);
             s.x += q.x;
             s.y += q.y;
             s.z += q.z;
@@ -539,87 +670,118 @@ __global__ void __launch_bounds__(256) router_sum_kernel(const SumArgs a)
         *reinterpret_cast<float4 *>(a.dw + (size_t)e * a.d + c) = s;
         return;
     }
-    // dbias: 32 experts a block, 8 threads of each
-    __shared__ double red[8][32];
-    const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
-    const int e = ((int)blockIdx.x - a.dw_blocks) * 32 + lane;
-    double s = 0.0;
-    if (e < a.E)
-        for (int b = row; b < a.bias_parts; b += 8)
-            s += a.bias_part[(size_t)b * a.E + e];
-    red[row][lane] = s;
-    __syncthreads();
-    if (row == 0 && e < a.E) {
-        for (int r = 1; r < 8; ++r)
-            s += red[r][lane];
-        a.dbias[e] = (float)s;
-    }
+    // dbias: a warp per expert
+    const int e = ((int)blockIdx.x - a.dw_blocks) * 8 + (threadIdx.x >> 5);
+    if (e >= a.E)
+        return;
+    float s = 0.0f;
+#pragma unroll 8
+    for (int b = threadIdx.x & 31; b < a.bias_parts; b += 32)
+        s += a.bias_part[(size_t)e * a.bias_parts + b];
+    s = warp_sum(s);
+    if ((threadIdx.x & 31) == 0)
+        a.dbias[e] = s;
 }
 
 // ---------------------------------------------------------------- dx = dl Wr (+ dx_add)
 
-// D[t][d']: M = 128 tokens, N = BN columns, K = e. A CTA keeps its BN columns of the router
-// weights' planes in shared memory (BN: as many of 256, 128, 64 as fit) and walks over token
-// tiles, whose planes of dl stream through a ring of [128 tokens][64 experts] units. A unit of
-// plane i meets the planes j <= planes - 1 - i of the weights. The work items are ordered columns
-// first, then tokens, and split evenly over the CTAs, so a CTA loads its weights once or twice.
-constexpr int kDxThreads = 192;
+// D[t][d']: M = 128 tokens, N = 64 nb columns, K = e.
+// Up to 64 experts (STREAM false) the pass is bound by memory: a CTA keeps its columns of
+// the router weights' planes in shared memory and walks over token tiles, whose planes of dl stream
+// through a ring of [128 tokens][64 experts] units; a unit of plane i meets the planes
+// j <= PLANES - 1 - i of the weights; eight epilogue warps. The CTAs of a group hold the column
+// slices of x and walk over the tokens together, so rows of dx are written whole within a
+// short time (measured against CTAs that each walk a strip of their own: 90 -> 74 us at
+// 32768 x 4096).
+// More experts (STREAM): the weights' planes do not fit beside the rest, so both operands stream,
+// 32 experts a stage, and a stage's products are all taken from it; tiles in token order over
+// the CTAs; four epilogue warps.
 constexpr int kUnit = 16384;   // 128 tokens x 64 experts, bf16
 constexpr int kPiece = 4096;   // 32 tokens x 128 bytes of dx: what one warp stores at a time
-constexpr int kSlots = 3;      // pieces of a warp in flight
-constexpr int kDxMaxB = 131072;
-constexpr int kDxUnits = 2;    // ring units, at least (as many as fit, at most kDxMaxUnits)
 constexpr int kDxMaxUnits = 6;
 constexpr int kDxMaxSmem = 231424;
 
+template <bool BF16, bool STREAM, bool ADD>
+struct DxTile {
+    static constexpr int PLANES = BF16 ? 2 : 3;
+    static constexpr int EW = STREAM ? 4 : 8;                  // epilogue warps
+    static constexpr int THREADS = 32 * (2 + EW);
+    // fp32 without dx_add: two pieces of a warp in flight and 256 columns a slice, with it three
+    // and 128 (32768 x 4096: 97 against 119 us, 190 against 236)
+    static constexpr int SLOTS = !BF16 && !STREAM && !ADD ? 2 : 3;
+    static constexpr int CP = BF16 ? 64 : 32;                  // columns of a piece
+    static constexpr int NB = !BF16 && !STREAM && ADD ? 2 : 4;  // boxes of a slice, at most
+    // dx_add's piece: loaded into the slot it leaves from (bf16), or beside it (half as wide)
+    static constexpr int ADD_SLOT = BF16 ? kPiece : kPiece / 2;
+    static constexpr int SLOT_AREA = EW * SLOTS * (kPiece + (ADD && !BF16 ? ADD_SLOT : 0));
+    __host__ __device__ static constexpr int unit(int nb)  // bytes of a ring unit
+    {
+        return STREAM ? PLANES * (8192 + nb * 4096) : kUnit;
+    }
+    __host__ __device__ static constexpr int weights(int nb) { return STREAM ? 0 : PLANES * nb * kBox; }
+};
+
 struct DxArgs {
     int N, d, E;
-    int chunks;     // of 64 experts
-    int bn;         // columns of a slice
+    int nb;         // boxes of 64 columns in a slice
     int slices;     // column slices
     int tiles;      // token tiles
     int units;      // ring units
-    int add;        // dx_add is given
     uint64_t timeout_ns;
 };
 
-__host__ __device__ inline int dx_piece_area(bool bf16)
+// K-major operand in 64-byte swizzled rows (8 rows x 64 bytes, atoms 512 bytes apart).
+__device__ __forceinline__ uint64_t smem_desc_sw64(uint32_t saddr)
 {
-    // a slot: the piece stored, and with fp32 dx the bf16 piece of dx_add beside it
-    return 4 * kSlots * (bf16 ? kPiece : kPiece + kPiece / 2);
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1u << 16) |
+           ((uint64_t)(512u >> 4) << 32) | ((uint64_t)1u << 46) | ((uint64_t)4u << 61);
 }
 
-template <bool BF16>
-__global__ void __launch_bounds__(kDxThreads, 1)
+template <bool BF16, bool STREAM, bool ADD>
+__global__ void __launch_bounds__((DxTile<BF16, STREAM, ADD>::THREADS), 1)
     router_dx_kernel(const __grid_constant__ CUtensorMap tm_dl,
                      const __grid_constant__ CUtensorMap tm_w,
                      const __grid_constant__ CUtensorMap tm_dx,
                      const __grid_constant__ CUtensorMap tm_add, const DxArgs a)
 {
-    constexpr int PLANES = BF16 ? 2 : 3;
-    constexpr int CP = BF16 ? 64 : 32;  // columns of a piece
+    using T = DxTile<BF16, STREAM, ADD>;
+    constexpr int PLANES = T::PLANES, CP = T::CP, SLOTS = T::SLOTS, EW = T::EW;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int nb = a.bn / 64, wbytes = PLANES * a.chunks * nb * kBox;
+    const int nb = a.nb, wbytes = T::weights(nb), ubytes = T::unit(nb);
     const uint32_t w_base = smem_u32(smem), a_base = w_base + wbytes;
-    const uint32_t p_base = a_base + a.units * kUnit;  // kPiece areas, then (fp32) dx_add's
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + wbytes + a.units * kUnit +
-                                                  dx_piece_area(BF16));
+    const uint32_t p_base = a_base + a.units * ubytes;  // pieces, then (fp32) dx_add's
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + wbytes + a.units * ubytes +
+                                                  T::SLOT_AREA);
     const uint32_t bar0 = smem_u32(bars);
     auto full = [&](int s) { return bar0 + 8u * s; };
     auto empty = [&](int s) { return bar0 + 8u * (kDxMaxUnits + s); };
     auto tfull = [&](int i) { return bar0 + 8u * (2 * kDxMaxUnits + i); };
     auto tempty = [&](int i) { return bar0 + 8u * (2 * kDxMaxUnits + 2 + i); };
     const uint32_t wfull = bar0 + 8u * (2 * kDxMaxUnits + 4);
-    const uint32_t wfree = bar0 + 8u * (2 * kDxMaxUnits + 5);
-    const uint32_t done = bar0 + 8u * (2 * kDxMaxUnits + 6);
-    auto addfull = [&](int w, int s) { return bar0 + 8u * (2 * kDxMaxUnits + 7 + w * kSlots + s); };
-    uint32_t *tmem_slot =
-        reinterpret_cast<uint32_t *>(bars + 2 * kDxMaxUnits + 7 + 4 * kSlots);
+    const uint32_t done = bar0 + 8u * (2 * kDxMaxUnits + 5);
+    auto addfull = [&](int w, int s) { return bar0 + 8u * (2 * kDxMaxUnits + 6 + w * SLOTS + s); };
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * kDxMaxUnits + 6 + EW * SLOTS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const Span span((int64_t)a.slices * a.tiles, gridDim.x, blockIdx.x);
+    // this CTA's tiles: item i is (token tile, column slice)
+    const int groups = gridDim.x / a.slices;  // STREAM false: a multiple
+    const int mine = STREAM ? (int)(((int64_t)a.tiles * a.slices - blockIdx.x + gridDim.x - 1) /
+                                    gridDim.x)
+                            : (a.tiles - (int)blockIdx.x / a.slices + groups - 1) / groups;
+    auto item = [&](int i, int &tile, int &slice) {
+        if constexpr (STREAM) {
+            const int64_t u = blockIdx.x + (int64_t)i * gridDim.x;
+            tile = (int)(u / a.slices);
+            slice = (int)(u - (int64_t)tile * a.slices);
+        } else {
+            tile = (int)blockIdx.x / a.slices + i * groups;
+            slice = (int)blockIdx.x % a.slices;
+        }
+    };
+    // ring units of one tile
+    const int per_tile = STREAM ? (a.E + 31) / 32 : PLANES;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kDxMaxUnits; ++s) {
@@ -628,13 +790,12 @@ __global__ void __launch_bounds__(kDxThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(tfull(i), 1);
-            mbar_init(tempty(i), 4);
+            mbar_init(tempty(i), EW);
         }
         mbar_init(wfull, 1);
-        mbar_init(wfree, 1);
         mbar_init(done, 1);
-        for (int i = 0; i < 4 * kSlots; ++i)
-            mbar_init(addfull(i / kSlots, i % kSlots), 1);
+        for (int i = 0; i < EW * SLOTS; ++i)
+            mbar_init(addfull(i / SLOTS, i % SLOTS), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         *abort_flag = 0;
     }
@@ -645,6 +806,8 @@ __global__ void __launch_bounds__(kDxThreads, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    grid_go();
+    grid_wait();  // the planes of the kernel before
     gg::tc_fence_before();
     __syncthreads();
     gg::tc_fence_after();
@@ -658,202 +821,206 @@ __global__ void __launch_bounds__(kDxThreads, 1)
             for (int s = 0; s < kDxMaxUnits; ++s)
                 issued[s] = false;
             bool ok = true;
-            int64_t have = -1;
-            int loads = 0;  // slices loaded
-            for (int64_t u = span.u0; u < span.u1 && ok; ++u) {
-                const int64_t slice = u / a.tiles, tile = u - slice * a.tiles;
-                if (slice != have) {
-                    // the weights of the next slice, once the MMAs of the last one are done
-                    if (loads > 0 && !gg::mbar_wait(wfree, (uint32_t)(loads - 1) & 1u, abort_flag,
-                                                    a.timeout_ns)) {
+            if constexpr (!STREAM) {
+                int tile, slice;
+                item(0, tile, slice);
+                mbar_arrive_expect_tx(wfull, wbytes);
+                tma_load_4d(w_base, &tm_w, 0, 0, slice * nb, 0, wfull);
+            }
+            for (int i = 0; i < mine && ok; ++i) {
+                int tile, slice;
+                item(i, tile, slice);
+                for (int u = 0; u < per_tile; ++u) {
+                    if (!gg::mbar_wait(empty(stage), phase ^ 1u, abort_flag, a.timeout_ns)) {
                         ok = false;
                         break;
                     }
-                    have = slice;
-                    ++loads;
-                    mbar_arrive_expect_tx(wfull, wbytes);
-                    for (int p = 0; p < PLANES; ++p)
-                        for (int c = 0; c < a.chunks; ++c)
-                            for (int b = 0; b < nb; ++b)
-                                tma_load_3d(w_base + ((p * a.chunks + c) * nb + b) * kBox, &tm_w,
-                                            (int)slice * a.bn + 64 * b, 64 * c, p, wfull);
-                }
-                for (int p = PLANES - 1; p >= 0 && ok; --p)
-                    for (int c = 0; c < a.chunks; ++c) {
-                        if (!gg::mbar_wait(empty(stage), phase ^ 1u, abort_flag, a.timeout_ns)) {
-                            ok = false;
-                            break;
-                        }
-                        mbar_arrive_expect_tx(full(stage), kUnit);
-                        tma_load_3d(a_base + stage * kUnit, &tm_dl, 64 * c, (int)tile * 128, p,
+                    const uint32_t dst = a_base + stage * ubytes;
+                    mbar_arrive_expect_tx(full(stage), ubytes);
+                    if constexpr (STREAM) {
+                        tma_load_3d(dst, &tm_dl, 32 * u, tile * 128, 0, full(stage));
+                        tma_load_4d(dst + PLANES * 8192, &tm_w, 0, 32 * u, slice * nb, 0,
                                     full(stage));
-                        issued[stage] = true;
-                        last[stage] = phase;
-                        if (++stage == a.units) {
-                            stage = 0;
-                            phase ^= 1u;
-                        }
+                    } else {
+                        tma_load_3d(dst, &tm_dl, 0, tile * 128, PLANES - 1 - u, full(stage));
                     }
+                    issued[stage] = true;
+                    last[stage] = phase;
+                    if (++stage == a.units) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
             }
             for (int s = 0; s < a.units; ++s)
                 if (issued[s])
                     gg::mbar_wait(full(s), last[s], abort_flag, a.timeout_ns, false);
-            if (loads > 0)
-                gg::mbar_wait(wfull, (uint32_t)(loads - 1) & 1u, abort_flag, a.timeout_ns, false);
+            if (!STREAM)
+                gg::mbar_wait(wfull, 0, abort_flag, a.timeout_ns, false);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t id = idesc(128, a.bn, false, true);
+        if (elect_one()) {
+            const uint32_t id = idesc(128, 64 * nb, false, true);
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
-            bool ok = true;
-            int64_t have = -1;
-            int loads = 0;
-            for (int64_t u = span.u0; u < span.u1 && ok; ++u) {
-                const int64_t slice = u / a.tiles;
-                if (slice != have) {
-                    if (!gg::mbar_wait(wfull, (uint32_t)loads & 1u, abort_flag, a.timeout_ns))
-                        break;
-                    have = slice;
-                    ++loads;
-                }
+            bool ok = STREAM || gg::mbar_wait(wfull, 0, abort_flag, a.timeout_ns);
+            for (int i = 0; i < mine && ok; ++i) {
                 if (!gg::mbar_wait(tempty(acc), acc_phase ^ 1u, abort_flag, a.timeout_ns))
                     break;
                 gg::tc_fence_after();
                 const uint32_t d0 = tmem + (uint32_t)(acc * 256);
                 uint32_t accumulate = 0;
-                for (int p = PLANES - 1; p >= 0 && ok; --p)
-                    for (int c = 0; c < a.chunks; ++c) {
-                        if (!gg::mbar_wait(full(stage), phase, abort_flag, a.timeout_ns)) {
-                            ok = false;
-                            break;
-                        }
-                        gg::tc_fence_after();
-                        const int ks = min(4, (a.E - 64 * c + 15) / 16);
-                        for (int j = PLANES - 1 - p; j >= 0; --j)
+                for (int u = 0; u < per_tile; ++u) {
+                    if (!gg::mbar_wait(full(stage), phase, abort_flag, a.timeout_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    gg::tc_fence_after();
+                    const uint32_t at = a_base + stage * ubytes;
+                    // the small products first; 16 experts are 32 bytes of a row of A and 2048
+                    // bytes of B (descriptor address units of 16 bytes)
+                    if constexpr (STREAM) {
+                        const int ks = min(2, (a.E - 32 * u + 15) / 16);
+#pragma unroll
+                        for (int order = PLANES - 1; order >= 0; --order)
+#pragma unroll
+                            for (int p = order; p >= 0; --p) {
+                                const uint64_t ad = smem_desc_sw64(at + p * 8192);
+                                const uint64_t bd = smem_desc_mn_sw128(
+                                    at + PLANES * 8192 + (order - p) * nb * 4096, 4096);
+                                gg::tc_mma<0>(d0, ad, bd, id, accumulate);
+                                accumulate = 1;
+                                if (ks > 1)
+                                    gg::tc_mma<0>(d0, ad + 2, bd + 128, id, 1u);
+                            }
+                    } else {
+                        const int ks = (a.E + 15) / 16;
+                        const uint64_t ad = gg::smem_desc_sw128(at);
+                        for (int j = u; j >= 0; --j) {
+                            const uint64_t bd = smem_desc_mn_sw128(w_base + j * nb * kBox, kBox);
                             for (int k = 0; k < ks; ++k) {
-                                gg::tc_mma<0>(
-                                    d0, gg::smem_desc_sw128(a_base + stage * kUnit + k * 32),
-                                    smem_desc_mn_sw128(
-                                        w_base + (j * a.chunks + c) * nb * kBox + k * 2048, kBox),
-                                    id, accumulate);
+                                gg::tc_mma<0>(d0, ad + 2 * k, bd + 128 * k, id, accumulate);
                                 accumulate = 1;
                             }
-                        gg::tc_commit(empty(stage));
-                        if (++stage == a.units) {
-                            stage = 0;
-                            phase ^= 1u;
                         }
                     }
+                    gg::tc_commit(empty(stage));
+                    if (++stage == a.units) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
                 if (!ok)
                     break;
                 gg::tc_commit(tfull(acc));
                 acc ^= 1;
                 if (acc == 0)
                     acc_phase ^= 1u;
-                if (u + 1 < span.u1 && (u + 1) / a.tiles != slice)
-                    gg::tc_commit(wfree);
             }
             gg::tc_commit(done);
             gg::mbar_wait(done, 0, abort_flag, a.timeout_ns, false);
         }
     } else {
-        // ---------------- epilogue: warps 2..5, TMEM lane quadrant = warp % 4
-        const int q = warp & 3;
+        // ---------------- epilogue: TMEM lane quadrant = warp % 4; the warps of a quadrant take
+        // turns at the pieces of a tile
+        constexpr int TURNS = EW / 4;
+        const int q = warp & 3, turn = (warp - 2) >> 2, w = warp - 2;
         const uint32_t lanes = (uint32_t)(q * 32) << 16;
-        const uint32_t slots = p_base + q * kSlots * kPiece;
-        const uint32_t adds = BF16 ? slots : p_base + 4 * kSlots * kPiece + q * kSlots * (kPiece / 2);
-        constexpr int ADD_SLOT = BF16 ? kPiece : kPiece / 2;
-        const int pieces = a.bn / CP;
-        const int64_t total = (span.u1 - span.u0) * pieces;
-        // piece i of this CTA: its column and its first token (of this warp's 32)
+        const uint32_t slots = p_base + w * SLOTS * kPiece;
+        const uint32_t adds = BF16 ? slots : p_base + EW * SLOTS * kPiece + w * SLOTS * T::ADD_SLOT;
+        const int pieces = 64 * nb / CP;                             // of a tile
+        const int own = (pieces - turn + TURNS - 1) / TURNS;         // of them, this warp's
+        const int64_t total = (int64_t)mine * own;
+        // this warp's piece i: its column and its first token (of the warp's 32)
         auto place = [&](int64_t i, int &col, int &row) {
-            const int64_t u = span.u0 + i / pieces, slice = u / a.tiles;
-            col = (int)slice * a.bn + (int)(i % pieces) * CP;
-            row = (int)(u - slice * a.tiles) * 128 + q * 32;
+            int tile, slice;
+            const int n = (int)(i / own);
+            item(n, tile, slice);
+            col = slice * 64 * nb + ((int)(i - (int64_t)n * own) * TURNS + turn) * CP;
+            row = tile * 128 + q * 32;
         };
         auto fetch = [&](int64_t i) {  // lane 0: dx_add's piece i into its slot
             int col, row;
             place(i, col, row);
-            const int s = (int)(i % kSlots);
-            mbar_arrive_expect_tx(addfull(q, s), ADD_SLOT);
-            gg::tma_load_2d(adds + s * ADD_SLOT, &tm_add, col, row, addfull(q, s));
+            const int s = (int)(i % SLOTS);
+            mbar_arrive_expect_tx(addfull(w, s), T::ADD_SLOT);
+            gg::tma_load_2d(adds + s * T::ADD_SLOT, &tm_add, col, row, addfull(w, s));
         };
         int64_t fetched = 0, used = 0;
-        if (a.add && lane == 0)
-            for (; fetched < total && fetched < kSlots - 1; ++fetched)
+        if (ADD && lane == 0)
+            for (; fetched < total && fetched < SLOTS - 1; ++fetched)
                 fetch(fetched);
         int acc = 0;
         uint32_t acc_phase = 0;
         int ok = 1;
-        for (int64_t u = span.u0; u < span.u1 && ok; ++u) {
+        for (int n = 0; n < mine && ok; ++n) {
             if (lane == 0)
                 ok = gg::mbar_wait(tfull(acc), acc_phase, abort_flag, a.timeout_ns) ? 1 : 0;
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok)
                 break;
             gg::tc_fence_after();
-            for (int pc = 0; pc < pieces; ++pc) {
-                const int64_t i = (u - span.u0) * pieces + pc;
-                const int s = (int)(i % kSlots);
+            for (int pc = 0; pc < own; ++pc) {
+                const int64_t i = (int64_t)n * own + pc;
+                const int s = (int)(i % SLOTS);
                 const uint32_t slot = slots + s * kPiece;
                 uint32_t v[CP];
 #pragma unroll
                 for (int c = 0; c < CP / 16; ++c)
-                    gg::tmem_ld16(tmem + lanes + acc * 256 + pc * CP + 16 * c,
+                    gg::tmem_ld16(tmem + lanes + acc * 256 + (pc * TURNS + turn) * CP + 16 * c,
                                   *reinterpret_cast<uint32_t(*)[16]>(v + 16 * c));
                 if (lane == 0) {
-                    if (a.add) {
-                        ok = gg::mbar_wait(addfull(q, s), (uint32_t)(i / kSlots) & 1u, abort_flag,
+                    if constexpr (ADD) {
+                        ok = gg::mbar_wait(addfull(w, s), (uint32_t)(i / SLOTS) & 1u, abort_flag,
                                            a.timeout_ns) ? 1 : 0;
                         if (ok)
                             ++used;
                     } else {
                         // the store that last read this slot has done so
-                        asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kSlots - 1) : "memory");
+                        asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(SLOTS - 1) : "memory");
                     }
                 }
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 gg::tmem_ld_wait();
                 if (!ok)
                     break;
-                if (a.add) {
+                if constexpr (ADD) {
 #pragma unroll
                     for (int c = 0; c < CP / 8; ++c) {
                         // 16 bytes = 8 columns; rows of 128 bytes (bf16 dx) or 64 bytes
-                        const uint32_t at = adds + s * ADD_SLOT +
+                        const uint32_t at = adds + s * T::ADD_SLOT +
                                             (BF16 ? lane * 128 + ((c ^ (lane & 7)) << 4)
                                                   : lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4));
-                        uint32_t w[4];
+                        uint32_t x[4];
                         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
                                      : "r"(at));
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             v[8 * c + 2 * j] = __float_as_uint(
-                                __uint_as_float(v[8 * c + 2 * j]) + bf16_lo(w[j]));
+                                __uint_as_float(v[8 * c + 2 * j]) + bf16_lo(x[j]));
                             v[8 * c + 2 * j + 1] = __float_as_uint(
-                                __uint_as_float(v[8 * c + 2 * j + 1]) + bf16_hi(w[j]));
+                                __uint_as_float(v[8 * c + 2 * j + 1]) + bf16_hi(x[j]));
                         }
                     }
                     if (!BF16 && lane == 0)  // the slot's last store has read it
-                        asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kSlots - 1) : "memory");
+                        asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(SLOTS - 1) : "memory");
                     __syncwarp();
                 }
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
-                    uint32_t w[4];
+                    uint32_t o[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         if constexpr (BF16)
-                            w[j] = pack_bf16x2(__uint_as_float(v[8 * c + 2 * j]),
+                            o[j] = pack_bf16x2(__uint_as_float(v[8 * c + 2 * j]),
                                                __uint_as_float(v[8 * c + 2 * j + 1]));
                         else
-                            w[j] = v[4 * c + j];
+                            o[j] = v[4 * c + j];
                     }
                     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
                                      slot + lane * 128 + ((c ^ (lane & 7)) << 4)),
-                                 "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                                 "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
                                  : "memory");
                 }
                 gg::fence_proxy_async_smem();
@@ -865,7 +1032,7 @@ __global__ void __launch_bounds__(kDxThreads, 1)
                         gg::tma_store_2d(&tm_dx, slot, col, row);
                     else
                         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                    if (a.add && fetched < total) {
+                    if (ADD && fetched < total) {
                         // into the slot before this one: its store has read it
                         if (BF16)
                             gg::bulk_wait_read1();
@@ -885,7 +1052,7 @@ __global__ void __launch_bounds__(kDxThreads, 1)
         }
         if (lane == 0) {
             for (; used < fetched; ++used)  // after a timeout: copies in flight have landed
-                gg::mbar_wait(addfull(q, (int)(used % kSlots)), (uint32_t)(used / kSlots) & 1u,
+                gg::mbar_wait(addfull(w, (int)(used % SLOTS)), (uint32_t)(used / SLOTS) & 1u,
                               abort_flag, a.timeout_ns, false);
             gg::bulk_wait_all();
         }
@@ -897,6 +1064,93 @@ __global__ void __launch_bounds__(kDxThreads, 1)
     if (warp == 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
                      : "memory");
+}
+
+// ---------------------------------------------------------------- few tokens
+
+// A call of at most kSmallTokens tokens and kSmallLogits logits, whole, in one launch: launches
+// are what such a call costs. A block takes 32 columns of x; every block makes dl (in shared
+// memory) for itself, then its columns of dx and dWr in fp32; block 0 also sums dbias.
+constexpr int kSmallTokens = 256;
+constexpr int kSmallLogits = 8192;
+constexpr int kSmallCols = 32;
+
+struct SmallArgs {
+    GradIn in;
+    const uint16_t *x;
+    const float *wr;
+    const uint16_t *add;
+    void *dx;
+    float *dw, *dbias;
+    int N, E, K, d, bf16;
+};
+
+constexpr int small_smem(int N, int E) { return 4 * (N * E + kSmallCols * (N + E)); }
+// The most a call takes: N + E is largest where one of them is (256 tokens, or 256 experts).
+constexpr int kSmallSmem = small_smem(kSmallTokens, kSmallLogits / kSmallTokens);
+static_assert(kSmallSmem == small_smem(kSmallLogits / 256, 256), "E <= 256");
+
+template <int LPR>
+__global__ void __launch_bounds__(256) router_small_grad_kernel(const SmallArgs a)
+{
+    extern __shared__ float small_smem_f[];
+    __shared__ __align__(16) float s_row[8 * 256];
+    constexpr int GW = 32 / LPR;
+    const int N = a.N, E = a.E, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    float *dl = small_smem_f, *xs = dl + N * E, *ws = xs + N * kSmallCols;  // [N][E] [N][32] [E][32]
+    const int col = blockIdx.x * kSmallCols + lane;
+    for (int t0 = warp * GW; t0 < N; t0 += 8 * GW) {
+        const int l = lane % LPR, t = t0 + lane / LPR;
+        float v[8];
+        token_dlogits<LPR>(a.in, N, E, a.K, t, l, s_row + warp * 256 + (lane / LPR) * (8 * LPR), v);
+        if (t < N) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (8 * l + j < E)
+                    dl[t * E + 8 * l + j] = v[j];
+        }
+    }
+    if (a.dw)
+        for (int t = warp; t < N; t += 8)
+            xs[t * kSmallCols + lane] =
+                col < a.d && (!a.in.mask || a.in.mask[t])
+                    ? __uint_as_float((uint32_t)a.x[(size_t)t * a.d + col] << 16)
+                    : 0.0f;
+    if (a.dx)
+        for (int e = warp; e < E; e += 8)
+            ws[e * kSmallCols + lane] = col < a.d ? a.wr[(size_t)e * a.d + col] : 0.0f;
+    __syncthreads();
+    if (a.dx && col < a.d) {
+        for (int t = warp; t < N; t += 8) {
+            float s = 0.0f;
+#pragma unroll 8
+            for (int e = 0; e < E; ++e)
+                s = fmaf(dl[t * E + e], ws[e * kSmallCols + lane], s);
+            const size_t at = (size_t)t * a.d + col;
+            if (a.add)
+                s += __uint_as_float((uint32_t)a.add[at] << 16);
+            if (a.bf16)
+                static_cast<uint16_t *>(a.dx)[at] = (uint16_t)pack_bf16x2(s, 0.0f);
+            else
+                static_cast<float *>(a.dx)[at] = s;
+        }
+    }
+    if (a.dw && col < a.d) {
+        for (int e = warp; e < E; e += 8) {
+            float s = 0.0f;
+#pragma unroll 8
+            for (int t = 0; t < N; ++t)
+                s = fmaf(dl[t * E + e], xs[t * kSmallCols + lane], s);
+            a.dw[(size_t)e * a.d + col] = s;
+        }
+    }
+    if (a.dbias && blockIdx.x == 0 && tid < E) {
+        float s = 0.0f;
+#pragma unroll 8
+        for (int t = 0; t < N; ++t)
+            s += dl[t * E + tid];
+        a.dbias[tid] = s;
+    }
 }
 
 }  // namespace rb
