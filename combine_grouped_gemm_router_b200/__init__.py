@@ -132,7 +132,9 @@ class _Lib:
     def __getattr__(self, name):
         if self._cdll is None:
             self._load()
-        return getattr(self._cdll, name)
+        fn = getattr(self._cdll, name)
+        self.__dict__[name] = fn  # found without this method from now on
+        return fn
 
 
 _lib = _Lib()
@@ -424,41 +426,54 @@ def moe_affinity_accumulate(N, E, K, topk_j, topk_j1, counts, stream=None):
 
 # ---------------------------------------------------------------- training
 
-def _expect(where, *wanted):
-    """Refuses (MoeError) a tensor the kernels would misread: each of ``wanted`` is (name, tensor,
-    dtypes, least number of elements). None and raw addresses pass."""
-    import torch
-    device = None
+def _args(where, stream, *wanted):
+    """The addresses of tensors, after refusing (MoeError) one that the kernels would misread:
+    each of ``wanted`` is (name, tensor, element types, least number of elements). None and raw
+    addresses pass. The last address is the stream's."""
+    device, out = -2, []
     for name, t, dtypes, least in wanted:
-        if t is None or isinstance(t, int):
+        if t is None or t.__class__ is int:
+            out.append(t)
             continue
         if t.dtype not in dtypes:
             raise MoeError(1, f"{where}: {name} is {t.dtype}, not {' or '.join(map(str, dtypes))}")
-        if not t.is_cuda:
-            raise MoeError(1, f"{where}: {name} is on {t.device}")
-        if device is None:
+        on = t.get_device()
+        if on != device:
+            if on < 0:
+                raise MoeError(1, f"{where}: {name} is on {t.device}")
+            import torch
             device = torch.cuda.current_device()
-        if t.get_device() != device:
-            raise MoeError(1, f"{where}: {name} is on {t.device}, the current device is "
-                              f"cuda:{device}")
+            if on != device:
+                raise MoeError(1, f"{where}: {name} is on {t.device}, the current device is "
+                                  f"cuda:{device}")
         if not t.is_contiguous():
             raise MoeError(1, f"{where}: {name} is not contiguous")
         if t.numel() < least:
             raise MoeError(1, f"{where}: {name} has {t.numel()} elements, {least} are needed")
+        out.append(t.data_ptr())
+    out.append(_stream(stream))
+    return out
 
 
-def _dtypes():
+class _Types:
     """Element types by the names the checks use (torch is imported on first use)."""
-    global _DTYPES
-    if _DTYPES is None:
+
+    def __getattr__(self, name):
         import torch
-        _DTYPES = {"f32": (torch.float32,), "i32": (torch.int32,), "bf16": (torch.bfloat16,),
-                   "f16": (torch.float16,), "u8": (torch.uint8,),
-                   "mask": (torch.uint8, torch.bool)}
-    return _DTYPES
+        self.f32, self.i32, self.bf16 = (torch.float32,), (torch.int32,), (torch.bfloat16,)
+        self.f16, self.u8 = (torch.float16,), (torch.uint8,)
+        self.mask = (torch.uint8, torch.bool)
+        self.any = (torch.uint8, torch.float32, torch.int32, torch.bfloat16, torch.float16)
+        if name not in self.__dict__:
+            raise AttributeError(name)
+        return self.__dict__[name]
 
 
-_DTYPES = None
+_T = _Types()
+
+
+def _bytes(ws):
+    return 0 if ws is None else ws.numel() * ws.element_size()
 
 
 def moe_balance_workspace_size(shape: MoeShape) -> int:
@@ -469,30 +484,26 @@ def moe_balance_loss(shape, logits, topk_idx, loss, counts, prob_mean, tokens, t
                      balance_coef=1.0, z_coef=0.0, ws=None, stream=None):
     """Balance loss and z-loss of the router: loss [3] = (total, balance, z), the per-expert
     counts [E], the mean probabilities [E] and the number of counted tokens [1]."""
-    d, N, E = _dtypes(), shape.N, shape.E
-    _expect("moe_balance_loss", ("logits", logits, d["f32"], N * E),
-            ("topk_idx", topk_idx, d["i32"], N * shape.K), ("loss", loss, d["f32"], 3),
-            ("counts", counts, d["i32"], E), ("prob_mean", prob_mean, d["f32"], E),
-            ("tokens", tokens, d["i32"], 1), ("token_mask", token_mask, d["mask"], N))
-    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
-    _check(_lib.moe_balance_loss(ctypes.byref(shape), _ptr(logits), _ptr(topk_idx),
-                                 _ptr(token_mask), balance_coef, z_coef, _ptr(loss),
-                                 _ptr(counts), _ptr(prob_mean), _ptr(tokens), _ptr(ws), ws_bytes,
-                                 _stream(stream)), "moe_balance_loss")
+    N, E = shape.N, shape.E
+    p = _args("moe_balance_loss", stream, ("logits", logits, _T.f32, N * E),
+              ("topk_idx", topk_idx, _T.i32, N * shape.K), ("token_mask", token_mask, _T.mask, N),
+              ("loss", loss, _T.f32, 3), ("counts", counts, _T.i32, E),
+              ("prob_mean", prob_mean, _T.f32, E), ("tokens", tokens, _T.i32, 1),
+              ("ws", ws, _T.any, 0))
+    _check(_lib.moe_balance_loss(ctypes.byref(shape), p[0], p[1], p[2], balance_coef, z_coef, p[3],
+                                 p[4], p[5], p[6], p[7], _bytes(ws), p[8]), "moe_balance_loss")
 
 
 def moe_balance_loss_backward(shape, logits, counts, tokens, dlogits, token_mask=None,
                               balance_coef=1.0, z_coef=0.0, dloss=None, stream=None):
     """dlogits [N, E]: the gradient of moe_balance_loss's total (times dloss [1], when given)."""
-    d, N, E = _dtypes(), shape.N, shape.E
-    _expect("moe_balance_loss_backward", ("logits", logits, d["f32"], N * E),
-            ("counts", counts, d["i32"], E), ("tokens", tokens, d["i32"], 1),
-            ("dlogits", dlogits, d["f32"], N * E), ("token_mask", token_mask, d["mask"], N),
-            ("dloss", dloss, d["f32"], 1))
-    _check(_lib.moe_balance_loss_backward(ctypes.byref(shape), _ptr(logits), _ptr(token_mask),
-                                          _ptr(counts), _ptr(tokens), balance_coef, z_coef,
-                                          _ptr(dloss), _ptr(dlogits), _stream(stream)),
-           "moe_balance_loss_backward")
+    N, E = shape.N, shape.E
+    p = _args("moe_balance_loss_backward", stream, ("logits", logits, _T.f32, N * E),
+              ("token_mask", token_mask, _T.mask, N), ("counts", counts, _T.i32, E),
+              ("tokens", tokens, _T.i32, 1), ("dloss", dloss, _T.f32, 1),
+              ("dlogits", dlogits, _T.f32, N * E))
+    _check(_lib.moe_balance_loss_backward(ctypes.byref(shape), p[0], p[1], p[2], p[3], balance_coef,
+                                          z_coef, p[4], p[5], p[6]), "moe_balance_loss_backward")
 
 
 def moe_route_backward_workspace_size(shape: MoeShape) -> int:
@@ -505,19 +516,17 @@ def moe_route_backward(shape, x, w_router, dx, dw_router, dbias=None, topk_idx=N
     """Backward pass of moe_route: from the gradients of the gate weights (dtopk_w, with topk_idx
     and topk_w) and of the logits (dlogits) to dx (fp32, or bf16 with out_bf16), dw_router and
     dbias."""
-    d, N, E, K = _dtypes(), shape.N, shape.E, shape.K
+    N, E, NK = shape.N, shape.E, shape.N * shape.K
     Nd, Ed = N * shape.d, E * shape.d
-    _expect("moe_route_backward", ("x", x, d["bf16"], Nd), ("w_router", w_router, d["f32"], Ed),
-            ("dx", dx, d["bf16" if shape.flags & MOE_FLAG_OUT_BF16 else "f32"], Nd),
-            ("dw_router", dw_router, d["f32"], Ed), ("dbias", dbias, d["f32"], E),
-            ("topk_idx", topk_idx, d["i32"], N * K), ("topk_w", topk_w, d["f32"], N * K),
-            ("dtopk_w", dtopk_w, d["f32"], N * K), ("dlogits", dlogits, d["f32"], N * E),
-            ("token_mask", token_mask, d["mask"], N), ("dx_add", dx_add, d["bf16"], Nd))
-    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
-    _check(_lib.moe_route_backward(ctypes.byref(shape), _ptr(x), _ptr(w_router), _ptr(topk_idx),
-                                   _ptr(topk_w), _ptr(dtopk_w), _ptr(dlogits), _ptr(token_mask),
-                                   _ptr(dx_add), _ptr(dx), _ptr(dw_router), _ptr(dbias), _ptr(ws),
-                                   ws_bytes, _stream(stream)), "moe_route_backward")
+    p = _args("moe_route_backward", stream, ("x", x, _T.bf16, Nd), ("w_router", w_router, _T.f32, Ed),
+              ("topk_idx", topk_idx, _T.i32, NK), ("topk_w", topk_w, _T.f32, NK),
+              ("dtopk_w", dtopk_w, _T.f32, NK), ("dlogits", dlogits, _T.f32, N * E),
+              ("token_mask", token_mask, _T.mask, N), ("dx_add", dx_add, _T.bf16, Nd),
+              ("dx", dx, _T.bf16 if shape.flags & MOE_FLAG_OUT_BF16 else _T.f32, Nd),
+              ("dw_router", dw_router, _T.f32, Ed), ("dbias", dbias, _T.f32, E),
+              ("ws", ws, _T.any, 0))
+    _check(_lib.moe_route_backward(ctypes.byref(shape), *p[:12], _bytes(ws), p[12]),
+           "moe_route_backward")
 
 
 def moe_checkpoint_bytes(shape: MoeShape) -> int:
@@ -534,29 +543,24 @@ def checkpoint_stride(shape: MoeShape) -> int:
 def moe_expert_up_checkpoint(shape, x_sorted, offsets, w1, w3, h, ckpt, stream=None):
     """moe_expert_up that also saves the pre-activations in 8 bits (ckpt: moe_checkpoint_bytes
     of uint8)."""
-    d, rows = _dtypes(), moe_rows_alloc(shape)
-    Efd = shape.E * shape.f * shape.d
-    _expect("moe_expert_up_checkpoint", ("x_sorted", x_sorted, d["bf16"], rows * shape.d),
-            ("offsets", offsets, d["i32"], shape.E + 1), ("w1", w1, d["bf16"], Efd),
-            ("w3", w3, d["bf16"], Efd),
-            ("h", h, d["bf16" if shape.flags & MOE_FLAG_H_BF16 else "f16"], rows * shape.f),
-            ("ckpt", ckpt, d["u8"], rows * checkpoint_stride(shape)))
-    _check(_lib.moe_expert_up_checkpoint(ctypes.byref(shape), _ptr(x_sorted), _ptr(offsets),
-                                         _ptr(w1), _ptr(w3), _ptr(h), _ptr(ckpt),
-                                         _stream(stream)), "moe_expert_up_checkpoint")
+    rows, Efd = moe_rows_alloc(shape), shape.E * shape.f * shape.d
+    p = _args("moe_expert_up_checkpoint", stream, ("x_sorted", x_sorted, _T.bf16, rows * shape.d),
+              ("offsets", offsets, _T.i32, shape.E + 1), ("w1", w1, _T.bf16, Efd),
+              ("w3", w3, _T.bf16, Efd),
+              ("h", h, _T.bf16 if shape.flags & MOE_FLAG_H_BF16 else _T.f16, rows * shape.f),
+              ("ckpt", ckpt, _T.u8, rows * checkpoint_stride(shape)))
+    _check(_lib.moe_expert_up_checkpoint(ctypes.byref(shape), *p), "moe_expert_up_checkpoint")
 
 
 def moe_swiglu_backward(shape, ckpt, offsets, dh, dgate, dup, h=None, stream=None):
     """Backward pass of the SwiGLU activation from its 8-bit checkpoint: dgate, dup and (when
     given) the recomputed h, all bf16, for the rows below offsets[E]."""
-    d, rows = _dtypes(), moe_rows_alloc(shape)
+    rows = moe_rows_alloc(shape)
     n = rows * shape.f
-    _expect("moe_swiglu_backward", ("ckpt", ckpt, d["u8"], rows * checkpoint_stride(shape)),
-            ("offsets", offsets, d["i32"], shape.E + 1), ("dh", dh, d["bf16"], n),
-            ("dgate", dgate, d["bf16"], n), ("dup", dup, d["bf16"], n), ("h", h, d["bf16"], n))
-    _check(_lib.moe_swiglu_backward(ctypes.byref(shape), _ptr(ckpt), _ptr(offsets), _ptr(dh),
-                                    _ptr(dgate), _ptr(dup), _ptr(h), _stream(stream)),
-           "moe_swiglu_backward")
+    p = _args("moe_swiglu_backward", stream, ("ckpt", ckpt, _T.u8, rows * checkpoint_stride(shape)),
+              ("offsets", offsets, _T.i32, shape.E + 1), ("dh", dh, _T.bf16, n),
+              ("dgate", dgate, _T.bf16, n), ("dup", dup, _T.bf16, n), ("h", h, _T.bf16, n))
+    _check(_lib.moe_swiglu_backward(ctypes.byref(shape), *p), "moe_swiglu_backward")
 
 
 # ---------------------------------------------------------------- host helpers

@@ -19,6 +19,7 @@ namespace moe {
 
 constexpr int kBalThreads = 1024;
 constexpr int kBalCols = 8;  // columns of a row held by one lane
+constexpr int kRows = 2;     // rows a lane group takes at once
 
 // Lane l of the LPR lanes of a row holds columns col(j), j = 0..7: two 16-byte chunks (VEC,
 // E % 4 == 0) or 8 columns LPR apart. A column at or past E reads as -inf (probability 0).
@@ -87,23 +88,31 @@ __device__ __forceinline__ float row_sum(float v)
     return v;
 }
 
-// Softmax of the row in v (in place: exponentials, not yet divided by the returned sum); m the
-// row's maximum.
+// Softmax of the row in v, in place: exponentials relative to the row's maximum, not yet divided
+// by their sum. Returns the sum; lse: the log-sum-exp. With L = log2(e), e^(v - m) is
+// 2^(v L - m L), one fused multiply-add: the rounding of m L is common to the row and cancels in
+// the probabilities. Results below fp32's normal range are 0.
 template <int LPR>
-__device__ __forceinline__ float row_softmax(float (&v)[8], float &m)
+__device__ __forceinline__ float row_softmax(float (&v)[8], float &lse)
 {
-    m = v[0];
+    constexpr float kL = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
+    float m = v[0];
 #pragma unroll
     for (int j = 1; j < 8; ++j)
         m = fmaxf(m, v[j]);
     m = row_max<LPR>(m);
+    const float c = -m * kL;
     float s = 0.0f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        v[j] = __expf(v[j] - m);
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(v[j]) : "f"(fmaf(v[j], kL, c)));
         s += v[j];
     }
-    return row_sum<LPR>(s);
+    s = row_sum<LPR>(s);
+    float l2;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(l2) : "f"(s));
+    lse = fmaf(l2, kLn2, m);
+    return s;
 }
 
 // One block's share of the sums, in the workspace: probability sums [blocks][E], counts
@@ -170,45 +179,70 @@ __global__ void __launch_bounds__(kBalThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int l = lane % LPR, grp = lane / LPR;
     const int E = out.E, K = out.K;
+    grid_go();
     if (tid < 256)
         s_count[tid] = 0;
     __syncthreads();
 
-    // counts: the block's share of the N*K assignments, in any order (integers)
-    const unsigned NK = (unsigned)N * (unsigned)K;
-    for (unsigned i = blockIdx.x * kBalThreads + tid; i < NK; i += gridDim.x * kBalThreads) {
-        const int e = topk_idx[i];
-        if (mask && !mask[i / (unsigned)K])
-            continue;
-        if ((unsigned)e < (unsigned)E)
-            atomicAdd(&s_count[e], 1);
-        else
-            set_dev_error(MOE_ERR_DEVICE_BOUNDS);
-    }
-
+    // kRows rows of a lane group at once: their loads are in flight together, and their shuffles
+    // fill each other's latency
     float acc[8] = {};
     float zsum = 0.0f;
     int m_tok = 0;
-    const int64_t stride = (int64_t)gridDim.x * WARPS * GW;
-    for (int64_t base = ((int64_t)blockIdx.x * WARPS + warp) * GW; base < N; base += stride) {
-        const int64_t t = base + grp;
-        const bool live = t < N && (!mask || mask[t]);
-        float v[8], m;
-        Slice::load(logits + (t < N ? t : 0) * E, live ? E : 0, l, v);
-        if (!live)
-            v[0] = 0.0f;  // keeps the arithmetic of a row left out finite
-        const float s = row_softmax<LPR>(v, m);
-        const float inv = live ? 1.0f / s : 0.0f;
+    bool bad_index = false, bad_logit = false;
+    const int64_t stride = (int64_t)gridDim.x * WARPS * GW * kRows;
+    for (int64_t base = ((int64_t)blockIdx.x * WARPS + warp) * GW * kRows; base < N;
+         base += stride) {
+        float v[kRows][8];
+        bool live[kRows];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            acc[j] += v[j] * inv;
-        if (live && l == 0) {
-            const float lse = m + logf(s);
-            if (!isfinite(lse))
-                set_dev_error(MOE_ERR_NONFINITE);
-            zsum += lse * lse;
-            ++m_tok;
+        for (int r = 0; r < kRows; ++r) {
+            const int64_t t = base + r * GW + grp;
+            live[r] = t < N && (!mask || mask[t]);
+            Slice::load(logits + (t < N ? t : 0) * E, t < N ? E : 0, l, v[r]);
         }
+        // counts: lane l takes the slots l, l + LPR, ... of its tokens
+        for (int k = l; k < K; k += LPR) {
+            int e[kRows];
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                const int64_t t = base + r * GW + grp;
+                e[r] = t < N ? topk_idx[t * K + k] : 0;
+            }
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                const bool ok = (unsigned)e[r] < (unsigned)E;
+                if (live[r] && ok)
+                    atomicAdd(&s_count[e[r]], 1);
+                bad_index |= live[r] && !ok;
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            if (!live[r]) {  // keeps the arithmetic of a row left out finite
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    v[r][j] = 0.0f;
+            }
+            float lse;
+            const float s = row_softmax<LPR>(v[r], lse);
+            const float inv = live[r] ? __fdividef(1.0f, s) : 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                acc[j] = fmaf(v[r][j], inv, acc[j]);
+            lse = live[r] ? lse : 0.0f;
+            bad_logit |= !isfinite(lse);
+            zsum = fmaf(lse, lse, zsum);
+            m_tok += live[r];
+        }
+    }
+    if (bad_index)
+        set_dev_error(MOE_ERR_DEVICE_BOUNDS);
+    if (bad_logit)
+        set_dev_error(MOE_ERR_NONFINITE);
+    if (l != 0) {  // every lane of a row has them
+        zsum = 0.0f;
+        m_tok = 0;
     }
 
     // over the row groups of the warp, then over the warps
@@ -256,56 +290,69 @@ __global__ void __launch_bounds__(kBalThreads, 1)
     }
 }
 
-// Adds up the blocks' shares, in block order within each of the threads of a column.
-__global__ void __launch_bounds__(kBalThreads, 1)
+// Adds up the blocks' shares: a cluster of 8 blocks, 32 experts each, 32 threads an expert (a
+// single block took 4 us longer to read the shares of 148 blocks). Every sum in a fixed order.
+constexpr int kFinishBlocks = 8;
+
+__global__ void __cluster_dims__(kFinishBlocks, 1, 1) __launch_bounds__(1024, 1)
     balance_finish_kernel(BalanceParts parts, int blocks, BalanceOut out)
 {
-    __shared__ double s_prob[kBalThreads];
-    __shared__ int s_count[kBalThreads];
-    __shared__ double s_red[32];
-    __shared__ double s_z;
-    __shared__ int s_m;
-    const int tid = threadIdx.x, E = out.E;
-    int ep = 1;
-    while (ep < E)
-        ep <<= 1;
-    const int e = tid & (ep - 1), part = tid / ep, np = kBalThreads / ep;
-    double p = 0.0;
-    int c = 0;
-    if (e < E) {
-#pragma unroll 8
-        for (int b = part; b < blocks; b += np) {
+    __shared__ double s_prob[32][33];
+    __shared__ int s_count[32][33];
+    __shared__ double s_term[kFinishBlocks];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, E = out.E;
+    const int e = blockIdx.x * 32 + lane;
+    grid_wait();
+    double p = 0.0, z = 0.0;
+    int c = 0, m = 0;
+    if (e < E)
+        for (int b = warp; b < blocks; b += 32) {
             p += parts.prob[(size_t)b * E + e];
             c += parts.count[(size_t)b * E + e];
         }
-    }
-    s_prob[tid] = p;
-    s_count[tid] = c;
-    if (tid < 32) {
-        double z = 0.0;
-        int mt = 0;
-        for (int b = tid; b < blocks; b += 32) {
+    s_prob[warp][lane] = p;
+    s_count[warp][lane] = c;
+    if (warp == 0) {
+        for (int b = lane; b < blocks; b += 32) {
             const float2 q = parts.zm[b];
             z += q.x;
-            mt += __float_as_int(q.y);
+            m += __float_as_int(q.y);
         }
         z = warp_sum(z);
-        mt = warp_sum(mt);
-        if (tid == 0) {
-            s_z = z;
-            s_m = mt;
-        }
+        m = warp_sum(m);
     }
     __syncthreads();
-    p = 0.0;
-    c = 0;
-    if (tid < E) {
-        for (int q = 0; q < np; ++q) {
-            p += s_prob[q * ep + tid];
-            c += s_count[q * ep + tid];
+    if (warp == 0) {
+        p = 0.0;
+        c = 0;
+        for (int w = 0; w < 32; ++w) {
+            p += s_prob[w][lane];
+            c += s_count[w][lane];
+        }
+        const double inv_m = m > 0 ? 1.0 / m : 0.0, mean = p * inv_m;
+        if (e < E) {
+            out.counts[e] = c;
+            out.prob_mean[e] = (float)mean;
+        }
+        const double term = warp_sum((double)c / out.K * inv_m * mean);
+        if (lane == 0) {  // to the first block
+            uint32_t at;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(smem_u32(&s_term[blockIdx.x])));
+            asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(at), "d"(term) : "memory");
         }
     }
-    balance_outputs(out, p, c, s_z, s_m, s_red);
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        double bal = 0.0;
+        for (int r = 0; r < kFinishBlocks; ++r)
+            bal += s_term[r];
+        const double inv_m = m > 0 ? 1.0 / m : 0.0, zz = z * inv_m;
+        bal *= E;
+        out.loss[0] = (float)(out.cb * bal + out.cz * zz);
+        out.loss[1] = (float)bal;
+        out.loss[2] = (float)zz;
+        out.tokens[0] = m;
+    }
 }
 
 // dlogits from the logits, the counts and the number of counted tokens.
@@ -330,29 +377,40 @@ __global__ void __launch_bounds__(256)
         const int c = Slice::col(l, j);
         f[j] = c < E ? (float)counts[c] * inv_m / (float)K : 0.0f;
     }
-    const int64_t stride = (int64_t)(gridDim.x * 256 / 32) * GW;
-    for (int64_t base = (int64_t)warp * GW; base < N; base += stride) {
-        const int64_t t = base + grp;
-        const bool live = t < N && (!mask || mask[t]);
-        float v[8], m;
-        Slice::load(logits + (t < N ? t : 0) * E, live ? E : 0, l, v);
-        if (!live)
-            v[0] = 0.0f;
-        const float s = row_softmax<LPR>(v, m);
-        float dot = 0.0f;
+    const int64_t stride = (int64_t)(gridDim.x * 256 / 32) * GW * kRows;
+    for (int64_t base = (int64_t)warp * GW * kRows; base < N; base += stride) {
+        float v[kRows][8];
+        bool live[kRows];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            dot += f[j] * v[j];
-        dot = row_sum<LPR>(dot);
-        const float inv = 1.0f / s;
-        const float inner = dot * inv, lterm = b * (m + logf(s));
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float p = v[j] * inv;
-            v[j] = live ? p * (a * (f[j] - inner) + lterm) : 0.0f;
+        for (int r = 0; r < kRows; ++r) {
+            const int64_t t = base + r * GW + grp;
+            live[r] = t < N && (!mask || mask[t]);
+            Slice::load(logits + (t < N ? t : 0) * E, t < N ? E : 0, l, v[r]);
         }
-        if (t < N)
-            Slice::store(dlogits + t * E, E, l, v);
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            const int64_t t = base + r * GW + grp;
+            if (!live[r]) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    v[r][j] = 0.0f;
+            }
+            float lse;
+            const float s = row_softmax<LPR>(v[r], lse);
+            float dot = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                dot += f[j] * v[r][j];
+            dot = row_sum<LPR>(dot);
+            const float inv = __fdividef(1.0f, s);
+            // p (a (f - inner) + b lse) = e (a f + c) / sum
+            const float c = b * lse - a * dot * inv;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[r][j] = live[r] ? v[r][j] * inv * (a * f[j] + c) : 0.0f;
+            if (t < N)
+                Slice::store(dlogits + t * E, E, l, v[r]);
+        }
     }
 }
 

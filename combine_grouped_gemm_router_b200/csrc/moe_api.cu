@@ -1137,13 +1137,13 @@ moe_status_t combine_impl(const moe_shape_t *s, const void *y, const int32_t *ro
 
 // Blocks of the balance sums: one per SM, and no more than give each warp a row. One block
 // takes a small call alone (and writes its outputs, without a second kernel).
-constexpr int64_t kBalSingle = 8192;  // logits of a call that one block takes
+constexpr int64_t kBalSingle = 32768;  // logits of a call that one block takes
 
 int balance_blocks(const moe_shape_t *s)
 {
     if ((int64_t)s->N * s->E <= kBalSingle)
         return 1;
-    const int64_t want = ((int64_t)s->N + 31) / 32;
+    const int64_t want = ((int64_t)s->N * s->E + 8191) / 8192;
     return (int)(want < num_sms() ? want : num_sms());
 }
 
@@ -1215,7 +1215,9 @@ moe_status_t balance_loss_impl(const moe_shape_t *s, const float *logits, const 
                 <<<blocks, kBalThreads, 0, st>>>(logits, topk_idx, mask, s->N, parts, out);
     });
     if (blocks > 1)
-        balance_finish_kernel<<<1, kBalThreads, 0, st>>>(parts, blocks, out);
+        if (launch_chained(balance_finish_kernel, kFinishBlocks, 1024, 0, st, parts, blocks, out) !=
+            cudaSuccess)
+            return MOE_ERR_CUDA;
     return launch_status();
 }
 
@@ -1226,7 +1228,7 @@ moe_status_t balance_grad_impl(const moe_shape_t *s, const float *logits, const 
     row_slices(s->E, [&](auto lpr, auto vec) {
         constexpr int LPR = decltype(lpr)::value;
         constexpr bool VEC = decltype(vec)::value;
-        const int64_t rows_per_block = 8 * (32 / LPR);
+        const int64_t rows_per_block = 8 * (32 / LPR) * kRows;
         const int64_t want = (s->N + rows_per_block - 1) / rows_per_block;
         const int64_t most = 8 * (int64_t)num_sms();
         balance_grad_kernel<LPR, VEC><<<(int)(want < most ? want : most), 256, 0, st>>>(
