@@ -277,21 +277,50 @@ int row_blocks(int N, int nchunks, int seg)
 
 
 // Launch that may overlap the end of the kernel before it on the stream (see grid_wait).
+// cluster: blocks of a cluster (1: none is asked for).
 template <typename... P, typename... A>
 cudaError_t launch_chained(void (*kern)(P...), int blocks, int threads, size_t smem,
-                           cudaStream_t st, A &&...args)
+                           cudaStream_t st, int cluster, A &&...args)
 {
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.gridDim = dim3(blocks, 1, 1);
     cfg.blockDim = dim3(threads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
+// Pairs of CTAs of a kernel that fit on the GPU at once (queried once per device), its shared
+// memory limit set on the way.
+template <typename Kernel>
+cudaError_t pairs_resident(Kernel kern, int threads, int smem, int *pairs)
+{
+    return once_per_device(reinterpret_cast<const void *>(kern), [&](int *n) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess)
+            return e;
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3(2 * (num_sms() / 2), 1, 1);
+        cfg.blockDim = dim3(threads, 1, 1);
+        cfg.dynamicSmemBytes = smem;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        return cudaOccupancyMaxActiveClusters(n, kern, &cfg);
+    }, pairs);
 }
 
 inline moe_status_t launch_status()
@@ -1215,7 +1244,7 @@ moe_status_t balance_loss_impl(const moe_shape_t *s, const float *logits, const 
                 <<<blocks, kBalThreads, 0, st>>>(logits, topk_idx, mask, s->N, parts, out);
     });
     if (blocks > 1)
-        if (launch_chained(balance_finish_kernel, kFinishBlocks, 1024, 0, st, parts, blocks, out) !=
+        if (launch_chained(balance_finish_kernel, kFinishBlocks, 1024, 0, st, 1, parts, blocks, out) !=
             cudaSuccess)
             return MOE_ERR_CUDA;
     return launch_status();
@@ -1253,21 +1282,20 @@ struct RouteBackLayout {
     size_t dl, wp, bias, part, total;
 };
 
-// dWr's tiles: `cols` columns of x by `rows` experts (padded); each tile's 128-token chunks in
+// dWr's tiles: 256 columns of x by 128 experts (or 64, folded); each tile's 128-token chunks in
 // `parts` equal shares, a CTA each.
 struct DwGeometry {
-    int ne, rows, cols, tiles, chunks, parts;
+    int tiles, groups, chunks, parts;
+    int blocks() const { return tiles * groups * parts; }
 };
 
 DwGeometry dw_geometry(const moe_shape_t *s)
 {
     DwGeometry g;
-    g.ne = (s->E + 63) / 64;
-    g.rows = g.ne > 2 ? 256 : 128;
-    g.cols = g.ne > 2 ? 128 : 256;
-    g.tiles = (s->d + g.cols - 1) / g.cols;
+    g.tiles = (s->d + 255) / 256;
+    g.groups = (s->E + 127) / 128;
     g.chunks = (s->N + rb::kChunk - 1) / rb::kChunk;
-    g.parts = num_sms() / g.tiles;
+    g.parts = num_sms() / (g.tiles * g.groups);
     if (g.parts > g.chunks)
         g.parts = g.chunks;
     if (g.parts < 1)
@@ -1299,7 +1327,7 @@ RouteBackLayout route_back_layout(const moe_shape_t *s)
     L.bias = o;
     o = align_up(o + (size_t)split_blocks(s) * s->E * 4);
     L.part = o;
-    o = align_up(o + (size_t)g.tiles * g.parts * g.rows * g.cols * 4);
+    o = align_up(o + (size_t)g.blocks() * 128 * 256 * 4);
     L.total = o;
     return L;
 }
@@ -1319,61 +1347,77 @@ bool make_tmap_box(CUtensorMap *m, CUtensorMapDataType dt, int rank, const void 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool BF16, bool STREAM, bool ADD>
+template <bool BF16, bool PAIR, bool ADD>
 moe_status_t launch_router_dx(const moe_shape_t *s, const uint16_t *dl, const uint16_t *wp,
                               const uint16_t *add, void *dx, cudaStream_t st)
 {
-    using T = rb::DxTile<BF16, STREAM, ADD>;
+    using T = rb::DxTile<BF16, PAIR, ADD>;
     const cuuint64_t N = (cuuint64_t)s->N, d = (cuuint64_t)s->d, E = (cuuint64_t)s->E;
     const cuuint64_t pitch = (cuuint64_t)dl_pitch_of(s);
-    CUtensorMap t_dl, t_w, t_dx, t_add;
+    CUtensorMap t_dl, t_w, t_dl1, t_w1, t_dx, t_add;
     const cuuint64_t dl_dims[3] = {E, N, 3}, dl_pitch[2] = {pitch * 2, N * pitch * 2};
     const cuuint64_t wb = (d + 63) / 64;  // boxes of columns
     const cuuint64_t w_dims[4] = {64, E, wb, 3}, w_pitch[3] = {128, E * 128, wb * E * 128};
     const cuuint64_t x_dims[2] = {d, N}, dx_pitch[1] = {d * (BF16 ? 2 : 4)}, add_pitch[1] = {d * 2};
-    const int nb = (s->d + 63) / 64 < T::NB ? (s->d + 63) / 64 : T::NB;
-    const cuuint32_t dl_box[3] = {STREAM ? 32 : 64, 128, STREAM ? T::PLANES : 1};
-    const cuuint32_t w_box[4] = {64, STREAM ? 32 : 64, (cuuint32_t)nb, T::PLANES};
+    int nb = (int)wb < T::NB ? (int)wb : T::NB;
+    if (PAIR)
+        nb = (nb + 1) & ~1;
+    const cuuint32_t dl_box[3] = {PAIR ? 32 : 64, 128, PAIR ? T::PLANES : 1};
+    const cuuint32_t w_box[4] = {64, PAIR ? 32 : 64, (cuuint32_t)(PAIR ? nb / 2 : nb), T::PLANES};
+    const cuuint32_t dl1_box[3] = {32, 128, 1}, w1_box[4] = {64, 32, (cuuint32_t)(nb / 2), 1};
     const cuuint32_t p_box[2] = {(cuuint32_t)T::CP, 32};
     const CUtensorMapDataType b16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const CUtensorMapSwizzle sw128 = CU_TENSOR_MAP_SWIZZLE_128B, sw64 = CU_TENSOR_MAP_SWIZZLE_64B;
-    if (!make_tmap_box(&t_dl, b16, 3, dl, dl_dims, dl_pitch, dl_box, STREAM ? sw64 : sw128) ||
+    if (!make_tmap_box(&t_dl, b16, 3, dl, dl_dims, dl_pitch, dl_box, PAIR ? sw64 : sw128) ||
         !make_tmap_box(&t_w, b16, 4, wp, w_dims, w_pitch, w_box, sw128) ||
         !make_tmap_box(&t_dx, BF16 ? b16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, dx, x_dims,
                        dx_pitch, p_box, sw128) ||
         (ADD && !make_tmap_box(&t_add, b16, 2, add, x_dims, add_pitch, p_box,
-                               BF16 ? sw128 : sw64)))
+                               BF16 ? sw128 : sw64)) ||
+        (PAIR && !BF16 &&
+         (!make_tmap_box(&t_dl1, b16, 3, dl, dl_dims, dl_pitch, dl1_box, sw64) ||
+          !make_tmap_box(&t_w1, b16, 4, wp, w_dims, w_pitch, w1_box, sw128))))
         return MOE_ERR_CUDA;
     if (!ADD)
         t_add = t_dx;  // not read
+    if (!PAIR || BF16) {
+        t_dl1 = t_dl;  // not read
+        t_w1 = t_w;
+    }
     rb::DxArgs a = {};
     a.N = s->N;
     a.d = s->d;
     a.E = s->E;
     a.nb = nb;
-    a.slices = (s->d + 64 * a.nb - 1) / (64 * a.nb);
-    a.tiles = (s->N + 127) / 128;
-    const int fixed = T::weights(a.nb) + T::SLOT_AREA + 1024 + 512;
-    a.units = (rb::kDxMaxSmem - fixed) / T::unit(a.nb);
+    a.slices = (s->d + 64 * nb - 1) / (64 * nb);
+    const int rows = PAIR ? 256 : 128;
+    a.tiles = (s->N + rows - 1) / rows;
+    const int fixed = T::weights(nb) + T::SLOT_AREA + 1024 + 512;
+    a.units = (rb::kDxMaxSmem - fixed) / T::unit(nb);
     if (a.units > rb::kDxMaxUnits)
         a.units = rb::kDxMaxUnits;
     a.timeout_ns = kWaitTimeoutNs;
-    int blocks;
-    if (STREAM) {
+    const size_t smem = fixed + a.units * T::unit(nb);
+    if constexpr (PAIR) {
+        const auto kern = rb::router_dx_pair_kernel<BF16, ADD>;
+        int pairs = 0;
+        if (pairs_resident(kern, T::THREADS, rb::kDxMaxSmem, &pairs) != cudaSuccess || pairs <= 0)
+            return MOE_ERR_CUDA;
         const int64_t items = (int64_t)a.slices * a.tiles;
-        blocks = (int)(items < num_sms() ? items : num_sms());
+        const int n = (int)(items < pairs ? items : pairs);
+        if (launch_chained(kern, 2 * n, T::THREADS, smem, st, 2, t_dl, t_w, t_dl1, t_w1, t_dx, t_add,
+                           a) != cudaSuccess)
+            return MOE_ERR_CUDA;
     } else {
+        const auto kern = rb::router_dx_kernel<BF16, ADD>;
         int groups = num_sms() / a.slices;
         if (groups > a.tiles)
             groups = a.tiles;
-        blocks = (groups < 1 ? 1 : groups) * a.slices;
+        if (smem_attr_once(kern, rb::kDxMaxSmem) != cudaSuccess ||
+            launch_chained(kern, (groups < 1 ? 1 : groups) * a.slices, T::THREADS, smem, st, 1, t_dl,
+                           t_w, t_dx, t_add, a) != cudaSuccess)
+            return MOE_ERR_CUDA;
     }
-    if (smem_attr_once(rb::router_dx_kernel<BF16, STREAM, ADD>, rb::kDxMaxSmem) != cudaSuccess)
-        return MOE_ERR_CUDA;
-    if (launch_chained(rb::router_dx_kernel<BF16, STREAM, ADD>, blocks, T::THREADS,
-                       fixed + a.units * T::unit(a.nb), st, t_dl, t_w, t_dx, t_add, a) !=
-        cudaSuccess)
-        return MOE_ERR_CUDA;
     return launch_status();
 }
 
@@ -1390,28 +1434,23 @@ moe_status_t launch_router_dw(const moe_shape_t *s, const DwGeometry &g, const u
     const cuuint64_t dl_pitch[3] = {pitch * 2, 128, N * pitch * 2};
     const cuuint64_t x_dims[2] = {d, N}, x_pitch[1] = {d * 2};
     const cuuint64_t xb_dims[3] = {64, N, d / 64}, xb_pitch[2] = {d * 2, 128};
-    const rb::DwArgs a{s->N, s->d, s->E, g.tiles, g.chunks, g.parts, x_boxes, mask, part,
+    const rb::DwArgs a{s->N, s->d, s->E, g.tiles, g.groups, g.chunks, g.parts, x_boxes, mask, part,
                        kWaitTimeoutNs};
-    auto go = [&](auto ne) {
-        using T = rb::DwTile<decltype(ne)::value>;
-        auto kern = rb::router_dw_kernel<decltype(ne)::value>;
-        const cuuint32_t x_box[3] = {64, T::TOK, T::XB}, dl_box[4] = {64, T::TOK, decltype(ne)::value, 3};
+    auto go = [&](auto fold) {
+        using T = rb::DwTile<decltype(fold)::value>;
+        auto kern = rb::router_dw_kernel<decltype(fold)::value>;
+        const cuuint32_t x_box[3] = {64, T::TOK, T::XB}, dl_box[4] = {64, T::TOK, T::NE, 3};
         CUtensorMap t_x, t_dl;
         if (!make_tmap_box(&t_x, b16, x_boxes ? 3 : 2, x, x_boxes ? xb_dims : x_dims,
                            x_boxes ? xb_pitch : x_pitch, x_box, sw128) ||
             !make_tmap_box(&t_dl, b16, 4, dl, dl_dims, dl_pitch, dl_box, sw128) ||
             smem_attr_once(kern, T::SMEM) != cudaSuccess ||
-            launch_chained(kern, g.tiles * g.parts, rb::kDwThreads, T::SMEM, st, t_x, t_dl, a) !=
+            launch_chained(kern, g.blocks(), rb::kDwThreads, T::SMEM, st, 1, t_x, t_dl, a) !=
                 cudaSuccess)
             return MOE_ERR_CUDA;
         return launch_status();
     };
-    switch (g.ne) {
-    case 1: return go(std::integral_constant<int, 1>{});
-    case 2: return go(std::integral_constant<int, 2>{});
-    case 3: return go(std::integral_constant<int, 3>{});
-    default: return go(std::integral_constant<int, 4>{});
-    }
+    return s->E <= 64 ? go(std::true_type{}) : go(std::false_type{});
 }
 
 moe_status_t route_backward_impl(const moe_shape_t *s, const RouteBackward &a, char *ws,
@@ -1467,9 +1506,8 @@ moe_status_t route_backward_impl(const moe_shape_t *s, const RouteBackward &a, c
     rb::SumArgs sum = {};
     sum.d = s->d;
     sum.E = s->E;
-    sum.tile_cols = g.cols;
-    sum.tile_rows = g.rows;
-    sum.fold = g.ne == 1;
+    sum.groups = g.groups;
+    sum.fold = s->E <= 64;
     sum.parts = g.parts;
     sum.part = part;
     sum.dw = a.dw;
@@ -1477,9 +1515,9 @@ moe_status_t route_backward_impl(const moe_shape_t *s, const RouteBackward &a, c
     sum.bias_part = bias;
     sum.bias_parts = sa.token_blocks;
     sum.dbias = a.dbias;
-    if (launch_chained(rb::router_sum_kernel, sum.dw_blocks + (a.dbias ? (s->E + 7) / 8 : 0), 256,
-                       0, st, sum) != cudaSuccess)
-        return MOE_ERR_CUDA;
+    // not chained: its blocks, scheduled early beside dWr's, cost more than the launch they hide
+    // (128 experts, 8192 x 2048: 52 against 48 us in all)
+    rb::router_sum_kernel<<<sum.dw_blocks + (a.dbias ? (s->E + 7) / 8 : 0), 256, 0, st>>>(sum);
     return launch_status();
 }
 

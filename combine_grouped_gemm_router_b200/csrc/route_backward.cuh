@@ -15,7 +15,8 @@
 //       2^-23 of the product); bf16: hi hi + hi mid + mid hi (below 2^-14, against the output's
 //       own rounding of 2^-8).
 // Four launches (one for a few tokens, router_small_grad_kernel): the split (router_split_grad_kernel), dx, dWr, and the sum of dWr's and dbias's
-// partial results in a fixed order, each scheduled while the one before it drains (grid_wait).
+// partial results in a fixed order; the middle two are scheduled while the one before them drains
+// (grid_wait).
 // No atomics: the same bits every run.
 #pragma once
 
@@ -319,13 +320,13 @@ __device__ __forceinline__ bool elect_one()
 
 // ---------------------------------------------------------------- dWr = dl^T x
 
-// D[e][d'] over a chunk of kChunk tokens: M = e (128 rows), N = d' (64 XB columns of x), K =
+// D[e][d'] over a chunk of kChunk tokens: M = e (128 rows), N = d' (256 columns of x), K =
 // tokens. Both operands lie in memory with the token as the slow index, so both are the
 // M/N-contiguous kind. e is M and d' is N because an M = 128 MMA costs 64 cycles however small
 // N is (measured: 70 at N = 64 and 128, 130 at 256: its A operand is read at 64 bytes a
-// cycle), so the wide side has to be N. Up to 64 experts, one M tile holds two planes (rows
-// e: hi and lo, rows 64 + e: mid), which router_sum_kernel adds; the fourth quarter of A is a box of
-// zeros. A chunk's sum is read back and added to fp32 registers before it is longer than 128
+// cycle), so the wide side has to be N. Up to 64 experts (FOLD), the M tile holds two planes
+// (rows e: hi and lo, rows 64 + e: mid), which router_sum_kernel adds; the fourth quarter of A is a
+// box of zeros. More experts: a CTA takes 128 of them. A chunk's sum is read back and added to fp32 registers before it is longer than 128
 // tokens: the tensor core's accumulator truncates, and a truncation per step over tens of
 // thousands of tokens would cost the low bits that the split keeps.
 // The CTAs of one share of the tokens walk over them together, one column tile each, so that
@@ -333,43 +334,43 @@ __device__ __forceinline__ bool elect_one()
 constexpr int kChunk = 128;  // tokens accumulated in TMEM
 constexpr int kDwThreads = 384;
 
-template <int NE>  // E rounded up to 64 NE
+template <bool FOLD>
 struct DwTile {
-    // tokens of a shared-memory stage. 64; 32 where two stages of 64 are all that fits (NE = 2:
-    // 57 -> 48 us at 16384 x 4096 x 128), though not where the zeroing of masked rows is what a
-    // stage waits for (NE = 1: 64 against 80 us with a mask at 32768 x 4096 x 64)
-    static constexpr int TOK = NE == 2 ? 32 : 64;
+    static constexpr int NE = FOLD ? 1 : 2;     // boxes of 64 experts
+    static constexpr int XB = 4;                // boxes of 64 columns of x
+    // tokens of a shared-memory stage. 64; 32 where two stages of 64 are all that fits (57 -> 48
+    // us at 16384 x 4096 x 128), though not where the zeroing of masked rows is what a stage
+    // waits for (FOLD: 64 against 80 us with a mask at 32768 x 4096 x 64)
+    static constexpr int TOK = FOLD ? 64 : 32;
     static constexpr int BOX = TOK * 128;       // a box of them: 64 columns
-    static constexpr int MT = NE > 2 ? 2 : 1;   // M tiles
-    static constexpr int XB = NE > 2 ? 2 : 4;   // boxes of 64 columns of x
     static constexpr int STAGE = (XB + 3 * NE) * BOX;
-    static constexpr int ZERO = NE % 2 ? BOX : 0;
-    static constexpr int FIT = (231168 - ZERO) / STAGE;  // within 227 KB
-    static constexpr int STAGES = FIT > 8 ? 8 : FIT;
+    static constexpr int ZERO = FOLD ? BOX : 0;
+    static constexpr int STAGES = (231168 - ZERO) / STAGE;  // within 227 KB
     static constexpr int SMEM = STAGES * STAGE + ZERO + 1024 + 256;
-    static_assert(STAGES >= 2, "tile");
+    static_assert(STAGES >= 2 && STAGES <= 8, "tile");
 };
 
 struct DwArgs {
     int N, d, E;
     int tiles;       // column tiles of 64 XB
+    int groups;      // groups of 128 experts (FOLD: 1)
     int chunks;      // chunks of kChunk tokens
     int parts;       // equal shares of the chunks, one CTA each for every tile
     int x_boxes;     // tm_x is [d / 64][N][64] (d % 64 == 0), else [N][d]
     const uint8_t *mask;
-    float *part;     // [tiles][parts][128 MT][64 XB]
+    float *part;     // [tiles][groups][parts][columns / 8][128 rows][8]
     uint64_t timeout_ns;
 };
 
 // Warps: 0 TMA, 1 MMA, 2 zeroes the rows of x of masked tokens (a masked row may hold NaN, and
 // 0 * NaN would reach every sum), 4..11 the running sums.
-template <int NE>
+template <bool FOLD>
 __global__ void __launch_bounds__(kDwThreads, 1)
     router_dw_kernel(const __grid_constant__ CUtensorMap tm_x,
                      const __grid_constant__ CUtensorMap tm_dl, const DwArgs a)
 {
-    using T = DwTile<NE>;
-    constexpr int S = T::STAGES, MT = T::MT, XB = T::XB, TOK = T::TOK, BOX = T::BOX;
+    using T = DwTile<FOLD>;
+    constexpr int S = T::STAGES, NE = T::NE, XB = T::XB, TOK = T::TOK, BOX = T::BOX;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -384,7 +385,9 @@ __global__ void __launch_bounds__(kDwThreads, 1)
     auto tempty = [&](int i) { return bar0 + 8u * (3 * S + 2 + i); };
     const uint32_t done = bar0 + 8u * (3 * S + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int tile = blockIdx.x % a.tiles, part = blockIdx.x / a.tiles;
+    // the CTAs that read the same tokens are neighbours, and of them those of the same columns
+    const int group = blockIdx.x % a.groups, tile = blockIdx.x / a.groups % a.tiles;
+    const int part = blockIdx.x / (a.groups * a.tiles);
     const int c0 = (int)((int64_t)a.chunks * part / a.parts);
     const int c1 = (int)((int64_t)a.chunks * (part + 1) / a.parts);
 
@@ -450,7 +453,7 @@ __global__ void __launch_bounds__(kDwThreads, 1)
                             gg::tma_load_2d(dst + b * BOX, &tm_x, (tile * XB + b) * 64, t0,
                                             full(stage));
                     // [plane][box of experts][token][64]
-                    tma_load_4d(dst + XB * BOX, &tm_dl, 0, t0, 0, 0, full(stage));
+                    tma_load_4d(dst + XB * BOX, &tm_dl, 0, t0, NE * group, 0, full(stage));
                     issued[stage] = true;
                     last[stage] = phase;
                     if (++stage == S) {
@@ -485,7 +488,7 @@ __global__ void __launch_bounds__(kDwThreads, 1)
                     const uint32_t xa = base + stage * T::STAGE, pb = xa + XB * BOX;
                     const uint64_t bdesc = smem_desc_mn_sw128(xa, BOX);
                     // 16 tokens are 2048 bytes: 128 of the descriptor's address units
-                    if constexpr (NE == 1) {
+                    if constexpr (FOLD) {
                         const uint64_t lo = smem_desc_mn_sw128(pb + 2 * BOX, zero - pb - 2 * BOX);
                         const uint64_t him = smem_desc_mn_sw128(pb, BOX);
 #pragma unroll
@@ -497,18 +500,13 @@ __global__ void __launch_bounds__(kDwThreads, 1)
                             gg::tc_mma<0>(d0, him + 128 * k, bdesc + 128 * k, id, 1u);
                     } else {
 #pragma unroll
-                        for (int p = 2; p >= 0; --p)
+                        for (int p = 2; p >= 0; --p) {
+                            const uint64_t adesc = smem_desc_mn_sw128(pb + p * NE * BOX, BOX);
 #pragma unroll
-                            for (int mt = 0; mt < MT; ++mt) {
-                                const uint32_t at = pb + (p * NE + 2 * mt) * BOX;
-                                const uint64_t adesc =
-                                    smem_desc_mn_sw128(at, 2 * mt + 1 < NE ? BOX : zero - at);
-#pragma unroll
-                                for (int k = 0; k < TOK / 16; ++k)
-                                    gg::tc_mma<0>(d0 + mt * 64 * XB, adesc + 128 * k,
-                                                  bdesc + 128 * k, id,
-                                                  (q > 0 || p < 2 || k > 0) ? 1u : 0u);
-                            }
+                            for (int k = 0; k < TOK / 16; ++k)
+                                gg::tc_mma<0>(d0, adesc + 128 * k, bdesc + 128 * k, id,
+                                              (q > 0 || p < 2 || k > 0) ? 1u : 0u);
+                        }
                     }
                     gg::tc_commit(empty(stage));
                     if (++stage == S) {
@@ -577,7 +575,7 @@ __global__ void __launch_bounds__(kDwThreads, 1)
         }
     } else if (warp >= 4) {
         // lane quadrant of TMEM: rows of D; the two warps of a quadrant take 128 of an
-        // accumulator's 256 columns each (with two M tiles: one tile each)
+        // accumulator's 256 columns each
         const int q = warp & 3, half = (warp - 4) >> 2;
         const uint32_t lanes = (uint32_t)(q * 32) << 16;
         float sum[128];
@@ -612,14 +610,18 @@ __global__ void __launch_bounds__(kDwThreads, 1)
             if (acc == 0)
                 acc_phase ^= 1u;
         }
-        const int row = (MT == 2 ? half * 128 : 0) + q * 32 + lane;
-        if ((NE == 1 ? (row & 63) : row) < a.E) {
-            float4 *dst = reinterpret_cast<float4 *>(
-                a.part + (((size_t)tile * a.parts + part) * (128 * MT) + row) * (64 * XB) +
-                (MT == 1 ? half * 128 : 0));
+        // 8 columns of a row are 32 bytes, and neighbouring rows are neighbours in memory: a warp
+        // writes 1 KB in one piece
+        const int row = q * 32 + lane;
+        if ((FOLD ? (row & 63) : group * 128 + row) < a.E) {
+            float *dst = a.part + ((size_t)(tile * a.groups + group) * a.parts + part) * (128 * 64 * XB) +
+                         (size_t)(half * 16) * 1024 + row * 8;
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                dst[j] = make_float4(sum[4 * j], sum[4 * j + 1], sum[4 * j + 2], sum[4 * j + 3]);
+            for (int j = 0; j < 16; ++j) {
+                float4 *o = reinterpret_cast<float4 *>(dst + j * 1024);
+                o[0] = make_float4(sum[8 * j], sum[8 * j + 1], sum[8 * j + 2], sum[8 * j + 3]);
+                o[1] = make_float4(sum[8 * j + 4], sum[8 * j + 5], sum[8 * j + 6], sum[8 * j + 7]);
+            }
         }
     }
     __syncwarp();
@@ -633,8 +635,8 @@ __global__ void __launch_bounds__(kDwThreads, 1)
 
 struct SumArgs {
     int d, E;
-    int tile_cols, tile_rows, parts;  // dWr's partial results [tiles][parts][tile_rows][tile_cols]
-    int fold;  // rows e and e + 64 of a partial result are both expert e's
+    int groups, parts;  // dWr's partial results [column tiles][groups][parts][32][128][8]
+    int fold;           // rows e and e + 64 of a partial result are both expert e's
     const float *part;
     float *dw;
     int dw_blocks;
@@ -643,31 +645,31 @@ struct SumArgs {
     float *dbias;
 };
 
-// dWr and dbias from their partial results, each element in the order of the tokens.
+// dWr and dbias from their partial results, each element in the order of the tokens. A thread takes
+// 4 columns of an expert; neighbouring threads: the other 4 of a group of 8, then the next expert
+// (as the results lie).
 __global__ void __launch_bounds__(256) router_sum_kernel(const SumArgs a)
 {
-    grid_wait();
     if ((int)blockIdx.x < a.dw_blocks) {
-        const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // 4 columns of one expert
-        const int64_t per_row = a.d / 4;
-        if (i >= per_row * a.E)
+        const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+        const int c8 = (int)(i / (2 * a.E)), r = (int)(i - (int64_t)c8 * (2 * a.E)), e = r >> 1;
+        if (c8 >= a.d / 8)
             return;
-        const int e = (int)(i / per_row), c = 4 * (int)(i - e * per_row);
-        const int tile = c / a.tile_cols;
-        const float *p = a.part + ((size_t)tile * a.parts * a.tile_rows + e) * a.tile_cols +
-                         (c - tile * a.tile_cols);
+        const int tile = c8 / 32, group = e / 128;
+        const float *p = a.part + (size_t)(tile * a.groups + group) * a.parts * 32768 +
+                         (size_t)(c8 - tile * 32) * 1024 + (e - group * 128) * 8 + (r & 1) * 4;
         float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        const int step = (a.fold ? 64 : a.tile_rows) * a.tile_cols;
-        const int n = a.fold ? 2 * a.parts : a.parts;  // with fold, rows 64 apart: tile_rows = 128
+        const int n = a.fold ? 2 * a.parts : a.parts;
 #pragma unroll 8
         for (int k = 0; k < n; ++k) {
-            const float4 q = *reinterpret_cast<const float4 *>(p + (size_t)k * step);
+            const float4 q = *reinterpret_cast<const float4 *>(
+                p + (a.fold ? (size_t)(k >> 1) * 32768 + (k & 1) * 512 : (size_t)k * 32768));
             s.x += q.x;
             s.y += q.y;
             s.z += q.z;
             s.w += q.w;
         }
-        *reinterpret_cast<float4 *>(a.dw + (size_t)e * a.d + c) = s;
+        *reinterpret_cast<float4 *>(a.dw + (size_t)e * a.d + 8 * c8 + (r & 1) * 4) = s;
         return;
     }
     // dbias: a warp per expert
@@ -686,66 +688,222 @@ __global__ void __launch_bounds__(256) router_sum_kernel(const SumArgs a)
 // ---------------------------------------------------------------- dx = dl Wr (+ dx_add)
 
 // D[t][d']: M = 128 tokens, N = 64 nb columns, K = e.
-// Up to 64 experts (STREAM false) the pass is bound by memory: a CTA keeps its columns of
+// Up to 64 experts (router_dx_kernel) the pass is bound by memory: a CTA keeps its columns of
 // the router weights' planes in shared memory and walks over token tiles, whose planes of dl stream
 // through a ring of [128 tokens][64 experts] units; a unit of plane i meets the planes
 // j <= PLANES - 1 - i of the weights; eight epilogue warps. The CTAs of a group hold the column
 // slices of x and walk over the tokens together, so rows of dx are written whole within a
 // short time (measured against CTAs that each walk a strip of their own: 90 -> 74 us at
 // 32768 x 4096).
-// More experts (STREAM): the weights' planes do not fit beside the rest, so both operands stream,
-// 32 experts a stage, and a stage's products are all taken from it; tiles in token order over
-// the CTAs; four epilogue warps.
+// More experts (router_dx_pair_kernel): the weights' planes do not fit beside the rest, so both
+// operands stream, 32 experts a stage. A pair of CTAs computes 256 tokens x 256 columns
+// (cta_group::2): each loads its 128 tokens of dl and half of the columns of the weights, which
+// both read.
 constexpr int kUnit = 16384;   // 128 tokens x 64 experts, bf16
 constexpr int kPiece = 4096;   // 32 tokens x 128 bytes of dx: what one warp stores at a time
 constexpr int kDxMaxUnits = 6;
 constexpr int kDxMaxSmem = 231424;
 
-template <bool BF16, bool STREAM, bool ADD>
+template <bool BF16, bool PAIR, bool ADD>
 struct DxTile {
     static constexpr int PLANES = BF16 ? 2 : 3;
-    static constexpr int EW = STREAM ? 4 : 8;                  // epilogue warps
+    static constexpr int EW = 8;                               // epilogue warps
     static constexpr int THREADS = 32 * (2 + EW);
-    // fp32 without dx_add: two pieces of a warp in flight and 256 columns a slice, with it three
-    // and 128 (32768 x 4096: 97 against 119 us, 190 against 236)
-    static constexpr int SLOTS = !BF16 && !STREAM && !ADD ? 2 : 3;
+    // pieces of a warp in flight. fp32, up to 64 experts: two and 256 columns a slice, with
+    // dx_add three and 128 (32768 x 4096: 97 against 119 us, 190 against 236)
+    static constexpr int SLOTS = BF16 || (!PAIR && ADD) ? 3 : 2;
     static constexpr int CP = BF16 ? 64 : 32;                  // columns of a piece
-    static constexpr int NB = !BF16 && !STREAM && ADD ? 2 : 4;  // boxes of a slice, at most
+    static constexpr int NB = !BF16 && !PAIR && ADD ? 2 : 4;   // boxes of a slice, at most
     // dx_add's piece: loaded into the slot it leaves from (bf16), or beside it (half as wide)
     static constexpr int ADD_SLOT = BF16 ? kPiece : kPiece / 2;
     static constexpr int SLOT_AREA = EW * SLOTS * (kPiece + (ADD && !BF16 ? ADD_SLOT : 0));
     __host__ __device__ static constexpr int unit(int nb)  // bytes of a ring unit
     {
-        return STREAM ? PLANES * (8192 + nb * 4096) : kUnit;
+        return PAIR ? PLANES * (8192 + nb / 2 * 4096) : kUnit;
     }
-    __host__ __device__ static constexpr int weights(int nb) { return STREAM ? 0 : PLANES * nb * kBox; }
+    __host__ __device__ static constexpr int weights(int nb) { return PAIR ? 0 : PLANES * nb * kBox; }
 };
 
 struct DxArgs {
     int N, d, E;
-    int nb;         // boxes of 64 columns in a slice
+    int nb;         // boxes of 64 columns in a slice (pairs: even)
     int slices;     // column slices
-    int tiles;      // token tiles
+    int tiles;      // token tiles of 128 (pairs: 256)
     int units;      // ring units
     uint64_t timeout_ns;
 };
 
-// K-major operand in 64-byte swizzled rows (8 rows x 64 bytes, atoms 512 bytes apart).
-__device__ __forceinline__ uint64_t smem_desc_sw64(uint32_t saddr)
+// The epilogue warps of both forms (warps 2 ..): TMEM lane quadrant = warp % 4; the warps of a
+// quadrant take turns at the pieces of a tile. item(i, tile, slice): this CTA's i-th tile of
+// `mine`; release(acc): the accumulator has been read.
+template <typename T, bool ADD, typename Item, typename Release>
+__device__ __forceinline__ void dx_epilogue(const DxArgs &a, uint32_t tmem, uint32_t p_base, int mine,
+                                            const CUtensorMap &tm_dx, const CUtensorMap &tm_add,
+                                            uint32_t tfull0, uint32_t addfull0,
+                                            volatile int *abort_flag, const Item &item,
+                                            const Release &release)
 {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1u << 16) |
-           ((uint64_t)(512u >> 4) << 32) | ((uint64_t)1u << 46) | ((uint64_t)4u << 61);
+    constexpr bool BF16 = T::PLANES == 2;
+    constexpr int CP = T::CP, SLOTS = T::SLOTS, EW = T::EW;
+    auto tfull = [&](int i) { return tfull0 + 8u * i; };
+    auto addfull = [&](int w, int s) { return addfull0 + 8u * (w * SLOTS + s); };
+    constexpr int TURNS = EW / 4;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int q = warp & 3, turn = (warp - 2) >> 2, w = warp - 2;
+    const int nb = a.nb;
+    const uint32_t lanes = (uint32_t)(q * 32) << 16;
+    const uint32_t slots = p_base + w * SLOTS * kPiece;
+    const uint32_t adds = BF16 ? slots : p_base + EW * SLOTS * kPiece + w * SLOTS * T::ADD_SLOT;
+    const int pieces = 64 * nb / CP;                             // of a tile
+    const int own = (pieces - turn + TURNS - 1) / TURNS;  // of them, this warp's
+    // a piece's column and first token (of the warp's 32); the pieces of a warp follow one
+    // another over the tiles, and their slots and barrier phases with them
+    struct Piece {
+        int n, pc, tile, slice, slot;
+        uint32_t phase;
+    };
+    auto col_of = [&](const Piece &p) { return p.slice * 64 * nb + (p.pc * TURNS + turn) * CP; };
+    auto row_of = [&](const Piece &p) { return p.tile * 128 + q * 32; };
+    auto next = [&](Piece &p) {
+        if (++p.slot == SLOTS) {
+            p.slot = 0;
+            p.phase ^= 1u;
+        }
+        if (++p.pc == own) {
+            p.pc = 0;
+            if (++p.n < mine)
+                item(p.n, p.tile, p.slice);
+        }
+    };
+    Piece now = {0, 0, 0, 0, 0, 0}, ahead;
+    item(0, now.tile, now.slice);
+    ahead = now;  // dx_add's piece to be fetched next (lane 0)
+    auto fetch = [&]() {
+        const uint32_t bar = addfull(w, ahead.slot);
+        mbar_arrive_expect_tx(bar, T::ADD_SLOT);
+        gg::tma_load_2d(adds + ahead.slot * T::ADD_SLOT, &tm_add, col_of(ahead), row_of(ahead), bar);
+        next(ahead);
+    };
+    int fetched = 0, used = 0;
+    if (ADD && lane == 0 && own > 0)
+        for (; ahead.n < mine && fetched < SLOTS - 1; ++fetched)
+            fetch();
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    int ok = 1;
+    for (int n = 0; n < mine && ok; ++n) {
+        if (lane == 0)
+            ok = gg::mbar_wait(tfull(acc), acc_phase, abort_flag, a.timeout_ns) ? 1 : 0;
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok)
+            break;
+        gg::tc_fence_after();
+        for (int pc = 0; pc < own; ++pc) {
+            const uint32_t slot = slots + now.slot * kPiece;
+            uint32_t v[CP];
+#pragma unroll
+            for (int c = 0; c < CP / 16; ++c)
+                gg::tmem_ld16(tmem + lanes + acc * 256 + (pc * TURNS + turn) * CP + 16 * c,
+                              *reinterpret_cast<uint32_t(*)[16]>(v + 16 * c));
+            if (lane == 0) {
+                if constexpr (ADD) {
+                    ok = gg::mbar_wait(addfull(w, now.slot), now.phase, abort_flag, a.timeout_ns)
+                             ? 1 : 0;
+                    if (ok)
+                        ++used;
+                } else {
+                    // the store that last read this slot has done so
+                    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(SLOTS - 1) : "memory");
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            gg::tmem_ld_wait();
+            if (!ok)
+                break;
+            if constexpr (ADD) {
+#pragma unroll
+                for (int c = 0; c < CP / 8; ++c) {
+                    // 16 bytes = 8 columns; rows of 128 bytes (bf16 dx) or 64 bytes
+                    const uint32_t at = adds + now.slot * T::ADD_SLOT +
+                                        (BF16 ? lane * 128 + ((c ^ (lane & 7)) << 4)
+                                              : lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4));
+                    uint32_t x[4];
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                                 : "r"(at));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        v[8 * c + 2 * j] = __float_as_uint(
+                            __uint_as_float(v[8 * c + 2 * j]) + bf16_lo(x[j]));
+                        v[8 * c + 2 * j + 1] = __float_as_uint(
+                            __uint_as_float(v[8 * c + 2 * j + 1]) + bf16_hi(x[j]));
+                    }
+                }
+                if (!BF16 && lane == 0)  // the slot's last store has read it
+                    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(SLOTS - 1) : "memory");
+                __syncwarp();
+            }
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                uint32_t o[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if constexpr (BF16)
+                        o[j] = pack_bf16x2(__uint_as_float(v[8 * c + 2 * j]),
+                                           __uint_as_float(v[8 * c + 2 * j + 1]));
+                    else
+                        o[j] = v[4 * c + j];
+                }
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                 slot + lane * 128 + ((c ^ (lane & 7)) << 4)),
+                             "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                             : "memory");
+            }
+            gg::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                const int col = col_of(now), row = row_of(now);
+                if (col < a.d && row < a.N)
+                    gg::tma_store_2d(&tm_dx, slot, col, row);
+                else
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                if (ADD && ahead.n < mine) {
+                    // into the slot before this one: its store has read it
+                    if (BF16)
+                        gg::bulk_wait_read1();
+                    fetch();
+                    ++fetched;
+                }
+            }
+            next(now);
+        }
+        gg::tc_fence_before();
+        __syncwarp();
+        if (!ok)
+            break;
+        if (lane == 0)
+            release(acc);
+        acc ^= 1;
+        if (acc == 0)
+            acc_phase ^= 1u;
+    }
+    if (lane == 0) {
+        for (; used < fetched; ++used)  // after a timeout: copies in flight have landed
+            gg::mbar_wait(addfull(w, used % SLOTS), (uint32_t)(used / SLOTS) & 1u, abort_flag,
+                          a.timeout_ns, false);
+        gg::bulk_wait_all();
+    }
 }
 
-template <bool BF16, bool STREAM, bool ADD>
-__global__ void __launch_bounds__((DxTile<BF16, STREAM, ADD>::THREADS), 1)
+template <bool BF16, bool ADD>
+__global__ void __launch_bounds__((DxTile<BF16, false, ADD>::THREADS), 1)
     router_dx_kernel(const __grid_constant__ CUtensorMap tm_dl,
                      const __grid_constant__ CUtensorMap tm_w,
                      const __grid_constant__ CUtensorMap tm_dx,
                      const __grid_constant__ CUtensorMap tm_add, const DxArgs a)
 {
-    using T = DxTile<BF16, STREAM, ADD>;
-    constexpr int PLANES = T::PLANES, CP = T::CP, SLOTS = T::SLOTS, EW = T::EW;
+    using T = DxTile<BF16, false, ADD>;
+    constexpr int PLANES = T::PLANES, SLOTS = T::SLOTS, EW = T::EW;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -761,27 +919,17 @@ __global__ void __launch_bounds__((DxTile<BF16, STREAM, ADD>::THREADS), 1)
     auto tempty = [&](int i) { return bar0 + 8u * (2 * kDxMaxUnits + 2 + i); };
     const uint32_t wfull = bar0 + 8u * (2 * kDxMaxUnits + 4);
     const uint32_t done = bar0 + 8u * (2 * kDxMaxUnits + 5);
-    auto addfull = [&](int w, int s) { return bar0 + 8u * (2 * kDxMaxUnits + 6 + w * SLOTS + s); };
+    const uint32_t addfull0 = bar0 + 8u * (2 * kDxMaxUnits + 6);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * kDxMaxUnits + 6 + EW * SLOTS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // this CTA's tiles: item i is (token tile, column slice)
-    const int groups = gridDim.x / a.slices;  // STREAM false: a multiple
-    const int mine = STREAM ? (int)(((int64_t)a.tiles * a.slices - blockIdx.x + gridDim.x - 1) /
-                                    gridDim.x)
-                            : (a.tiles - (int)blockIdx.x / a.slices + groups - 1) / groups;
+    const int groups = gridDim.x / a.slices, group = blockIdx.x / a.slices;
+    const int mine = (a.tiles - group + groups - 1) / groups;
     auto item = [&](int i, int &tile, int &slice) {
-        if constexpr (STREAM) {
-            const int64_t u = blockIdx.x + (int64_t)i * gridDim.x;
-            tile = (int)(u / a.slices);
-            slice = (int)(u - (int64_t)tile * a.slices);
-        } else {
-            tile = (int)blockIdx.x / a.slices + i * groups;
-            slice = (int)blockIdx.x % a.slices;
-        }
+        tile = group + i * groups;
+        slice = blockIdx.x % a.slices;
     };
-    // ring units of one tile
-    const int per_tile = STREAM ? (a.E + 31) / 32 : PLANES;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kDxMaxUnits; ++s) {
@@ -795,7 +943,7 @@ __global__ void __launch_bounds__((DxTile<BF16, STREAM, ADD>::THREADS), 1)
         mbar_init(wfull, 1);
         mbar_init(done, 1);
         for (int i = 0; i < EW * SLOTS; ++i)
-            mbar_init(addfull(i / SLOTS, i % SLOTS), 1);
+            mbar_init(addfull0 + 8u * i, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         *abort_flag = 0;
     }
@@ -821,29 +969,19 @@ __global__ void __launch_bounds__((DxTile<BF16, STREAM, ADD>::THREADS), 1)
             for (int s = 0; s < kDxMaxUnits; ++s)
                 issued[s] = false;
             bool ok = true;
-            if constexpr (!STREAM) {
-                int tile, slice;
-                item(0, tile, slice);
-                mbar_arrive_expect_tx(wfull, wbytes);
-                tma_load_4d(w_base, &tm_w, 0, 0, slice * nb, 0, wfull);
-            }
+            mbar_arrive_expect_tx(wfull, wbytes);
+            tma_load_4d(w_base, &tm_w, 0, 0, (int)(blockIdx.x % a.slices) * nb, 0, wfull);
             for (int i = 0; i < mine && ok; ++i) {
                 int tile, slice;
                 item(i, tile, slice);
-                for (int u = 0; u < per_tile; ++u) {
+                for (int u = 0; u < PLANES; ++u) {
                     if (!gg::mbar_wait(empty(stage), phase ^ 1u, abort_flag, a.timeout_ns)) {
                         ok = false;
                         break;
                     }
                     const uint32_t dst = a_base + stage * ubytes;
                     mbar_arrive_expect_tx(full(stage), ubytes);
-                    if constexpr (STREAM) {
-                        tma_load_3d(dst, &tm_dl, 32 * u, tile * 128, 0, full(stage));
-                        tma_load_4d(dst + PLANES * 8192, &tm_w, 0, 32 * u, slice * nb, 0,
-                                    full(stage));
-                    } else {
-                        tma_load_3d(dst, &tm_dl, 0, tile * 128, PLANES - 1 - u, full(stage));
-                    }
+                    tma_load_3d(dst, &tm_dl, 0, tile * 128, PLANES - 1 - u, full(stage));
                     issued[stage] = true;
                     last[stage] = phase;
                     if (++stage == a.units) {
@@ -855,22 +993,21 @@ __global__ void __launch_bounds__((DxTile<BF16, STREAM, ADD>::THREADS), 1)
             for (int s = 0; s < a.units; ++s)
                 if (issued[s])
                     gg::mbar_wait(full(s), last[s], abort_flag, a.timeout_ns, false);
-            if (!STREAM)
-                gg::mbar_wait(wfull, 0, abort_flag, a.timeout_ns, false);
+            gg::mbar_wait(wfull, 0, abort_flag, a.timeout_ns, false);
         }
     } else if (warp == 1) {
         if (elect_one()) {
             const uint32_t id = idesc(128, 64 * nb, false, true);
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
-            bool ok = STREAM || gg::mbar_wait(wfull, 0, abort_flag, a.timeout_ns);
+            bool ok = gg::mbar_wait(wfull, 0, abort_flag, a.timeout_ns);
             for (int i = 0; i < mine && ok; ++i) {
                 if (!gg::mbar_wait(tempty(acc), acc_phase ^ 1u, abort_flag, a.timeout_ns))
                     break;
                 gg::tc_fence_after();
                 const uint32_t d0 = tmem + (uint32_t)(acc * 256);
                 uint32_t accumulate = 0;
-                for (int u = 0; u < per_tile; ++u) {
+                for (int u = 0; u < PLANES; ++u) {
                     if (!gg::mbar_wait(full(stage), phase, abort_flag, a.timeout_ns)) {
                         ok = false;
                         break;
@@ -879,29 +1016,13 @@ __global__ void __launch_bounds__((DxTile<BF16, STREAM, ADD>::THREADS), 1)
                     const uint32_t at = a_base + stage * ubytes;
                     // the small products first; 16 experts are 32 bytes of a row of A and 2048
                     // bytes of B (descriptor address units of 16 bytes)
-                    if constexpr (STREAM) {
-                        const int ks = min(2, (a.E - 32 * u + 15) / 16);
-#pragma unroll
-                        for (int order = PLANES - 1; order >= 0; --order)
-#pragma unroll
-                            for (int p = order; p >= 0; --p) {
-                                const uint64_t ad = smem_desc_sw64(at + p * 8192);
-                                const uint64_t bd = smem_desc_mn_sw128(
-                                    at + PLANES * 8192 + (order - p) * nb * 4096, 4096);
-                                gg::tc_mma<0>(d0, ad, bd, id, accumulate);
-                                accumulate = 1;
-                                if (ks > 1)
-                                    gg::tc_mma<0>(d0, ad + 2, bd + 128, id, 1u);
-                            }
-                    } else {
-                        const int ks = (a.E + 15) / 16;
-                        const uint64_t ad = gg::smem_desc_sw128(at);
-                        for (int j = u; j >= 0; --j) {
-                            const uint64_t bd = smem_desc_mn_sw128(w_base + j * nb * kBox, kBox);
-                            for (int k = 0; k < ks; ++k) {
-                                gg::tc_mma<0>(d0, ad + 2 * k, bd + 128 * k, id, accumulate);
-                                accumulate = 1;
-                            }
+                    const int ks = (a.E + 15) / 16;
+                    const uint64_t ad = gg::smem_desc_sw128(at);
+                    for (int j = u; j >= 0; --j) {
+                        const uint64_t bd = smem_desc_mn_sw128(w_base + j * nb * kBox, kBox);
+                        for (int k = 0; k < ks; ++k) {
+                            gg::tc_mma<0>(d0, ad + 2 * k, bd + 128 * k, id, accumulate);
+                            accumulate = 1;
                         }
                     }
                     gg::tc_commit(empty(stage));
@@ -921,141 +1042,8 @@ __global__ void __launch_bounds__((DxTile<BF16, STREAM, ADD>::THREADS), 1)
             gg::mbar_wait(done, 0, abort_flag, a.timeout_ns, false);
         }
     } else {
-        // ---------------- epilogue: TMEM lane quadrant = warp % 4; the warps of a quadrant take
-        // turns at the pieces of a tile
-        constexpr int TURNS = EW / 4;
-        const int q = warp & 3, turn = (warp - 2) >> 2, w = warp - 2;
-        const uint32_t lanes = (uint32_t)(q * 32) << 16;
-        const uint32_t slots = p_base + w * SLOTS * kPiece;
-        const uint32_t adds = BF16 ? slots : p_base + EW * SLOTS * kPiece + w * SLOTS * T::ADD_SLOT;
-        const int pieces = 64 * nb / CP;                             // of a tile
-        const int own = (pieces - turn + TURNS - 1) / TURNS;         // of them, this warp's
-        const int64_t total = (int64_t)mine * own;
-        // this warp's piece i: its column and its first token (of the warp's 32)
-        auto place = [&](int64_t i, int &col, int &row) {
-            int tile, slice;
-            const int n = (int)(i / own);
-            item(n, tile, slice);
-            col = slice * 64 * nb + ((int)(i - (int64_t)n * own) * TURNS + turn) * CP;
-            row = tile * 128 + q * 32;
-        };
-        auto fetch = [&](int64_t i) {  // lane 0: dx_add's piece i into its slot
-            int col, row;
-            place(i, col, row);
-            const int s = (int)(i % SLOTS);
-            mbar_arrive_expect_tx(addfull(w, s), T::ADD_SLOT);
-            gg::tma_load_2d(adds + s * T::ADD_SLOT, &tm_add, col, row, addfull(w, s));
-        };
-        int64_t fetched = 0, used = 0;
-        if (ADD && lane == 0)
-            for (; fetched < total && fetched < SLOTS - 1; ++fetched)
-                fetch(fetched);
-        int acc = 0;
-        uint32_t acc_phase = 0;
-        int ok = 1;
-        for (int n = 0; n < mine && ok; ++n) {
-            if (lane == 0)
-                ok = gg::mbar_wait(tfull(acc), acc_phase, abort_flag, a.timeout_ns) ? 1 : 0;
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (!ok)
-                break;
-            gg::tc_fence_after();
-            for (int pc = 0; pc < own; ++pc) {
-                const int64_t i = (int64_t)n * own + pc;
-                const int s = (int)(i % SLOTS);
-                const uint32_t slot = slots + s * kPiece;
-                uint32_t v[CP];
-#pragma unroll
-                for (int c = 0; c < CP / 16; ++c)
-                    gg::tmem_ld16(tmem + lanes + acc * 256 + (pc * TURNS + turn) * CP + 16 * c,
-                                  *reinterpret_cast<uint32_t(*)[16]>(v + 16 * c));
-                if (lane == 0) {
-                    if constexpr (ADD) {
-                        ok = gg::mbar_wait(addfull(w, s), (uint32_t)(i / SLOTS) & 1u, abort_flag,
-                                           a.timeout_ns) ? 1 : 0;
-                        if (ok)
-                            ++used;
-                    } else {
-                        // the store that last read this slot has done so
-                        asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(SLOTS - 1) : "memory");
-                    }
-                }
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-                gg::tmem_ld_wait();
-                if (!ok)
-                    break;
-                if constexpr (ADD) {
-#pragma unroll
-                    for (int c = 0; c < CP / 8; ++c) {
-                        // 16 bytes = 8 columns; rows of 128 bytes (bf16 dx) or 64 bytes
-                        const uint32_t at = adds + s * T::ADD_SLOT +
-                                            (BF16 ? lane * 128 + ((c ^ (lane & 7)) << 4)
-                                                  : lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4));
-                        uint32_t x[4];
-                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                                     : "r"(at));
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            v[8 * c + 2 * j] = __float_as_uint(
-                                __uint_as_float(v[8 * c + 2 * j]) + bf16_lo(x[j]));
-                            v[8 * c + 2 * j + 1] = __float_as_uint(
-                                __uint_as_float(v[8 * c + 2 * j + 1]) + bf16_hi(x[j]));
-                        }
-                    }
-                    if (!BF16 && lane == 0)  // the slot's last store has read it
-                        asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(SLOTS - 1) : "memory");
-                    __syncwarp();
-                }
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    uint32_t o[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if constexpr (BF16)
-                            o[j] = pack_bf16x2(__uint_as_float(v[8 * c + 2 * j]),
-                                               __uint_as_float(v[8 * c + 2 * j + 1]));
-                        else
-                            o[j] = v[4 * c + j];
-                    }
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                     slot + lane * 128 + ((c ^ (lane & 7)) << 4)),
-                                 "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
-                                 : "memory");
-                }
-                gg::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    int col, row;
-                    place(i, col, row);
-                    if (col < a.d && row < a.N)
-                        gg::tma_store_2d(&tm_dx, slot, col, row);
-                    else
-                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                    if (ADD && fetched < total) {
-                        // into the slot before this one: its store has read it
-                        if (BF16)
-                            gg::bulk_wait_read1();
-                        fetch(fetched++);
-                    }
-                }
-            }
-            gg::tc_fence_before();
-            __syncwarp();
-            if (!ok)
-                break;
-            if (lane == 0)
-                mbar_arrive(tempty(acc));
-            acc ^= 1;
-            if (acc == 0)
-                acc_phase ^= 1u;
-        }
-        if (lane == 0) {
-            for (; used < fetched; ++used)  // after a timeout: copies in flight have landed
-                gg::mbar_wait(addfull(w, (int)(used % SLOTS)), (uint32_t)(used / SLOTS) & 1u,
-                              abort_flag, a.timeout_ns, false);
-            gg::bulk_wait_all();
-        }
+        dx_epilogue<T, ADD>(a, tmem, p_base, mine, tm_dx, tm_add, tfull(0), addfull0, abort_flag,
+                            item, [&](int acc) { mbar_arrive(tempty(acc)); });
     }
     __syncwarp();
     gg::tc_fence_before();
@@ -1063,6 +1051,244 @@ __global__ void __launch_bounds__((DxTile<BF16, STREAM, ADD>::THREADS), 1)
     gg::tc_fence_after();
     if (warp == 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
+                     : "memory");
+}
+
+// K-major operand in 64-byte swizzled rows (8 rows x 64 bytes, atoms 512 bytes apart).
+__device__ __forceinline__ uint64_t smem_desc_sw64(uint32_t saddr)
+{
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1u << 16) |
+           ((uint64_t)(512u >> 4) << 32) | ((uint64_t)1u << 46) | ((uint64_t)4u << 61);
+}
+
+// TMA loads and commits of a pair (no multicast): each CTA loads into its own shared memory, and
+// the bytes count on the first CTA's barrier.
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap *map, int x, int y,
+                                                 int z, uint32_t bar_cluster_addr)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar_cluster_addr)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const CUtensorMap *map, int x, int y,
+                                                 int z, int w, uint32_t bar_cluster_addr)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar_cluster_addr)
+        : "memory");
+}
+
+// A stage of a tile (chunk = 32 experts). Products of two planes i, j: those below fp32's
+// rounding, i + j >= PLANES, are left out. bf16 dx: stage u holds both planes of chunk u and
+// gives all three products. fp32 dx: stages 0 .. C-1 hold the three planes of a chunk and give the
+// five products below hi hi; the stages after them hold the hi planes of three chunks each and
+// give hi hi. So the accumulator, which the tensor core truncates at every step, holds small
+// values until E / 16 steps before the end (all six products chunk by chunk left a relative
+// error of 1.5e-6 with 256 experts).
+template <bool BF16, bool ADD>
+__global__ void __launch_bounds__((DxTile<BF16, true, ADD>::THREADS), 1)
+    router_dx_pair_kernel(const __grid_constant__ CUtensorMap tm_dl,
+                          const __grid_constant__ CUtensorMap tm_w,
+                          const __grid_constant__ CUtensorMap tm_dl1,
+                          const __grid_constant__ CUtensorMap tm_w1,
+                          const __grid_constant__ CUtensorMap tm_dx,
+                          const __grid_constant__ CUtensorMap tm_add, const DxArgs a)
+{
+    using T = DxTile<BF16, true, ADD>;
+    constexpr int PLANES = T::PLANES, SLOTS = T::SLOTS, EW = T::EW;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int hb = a.nb / 2, ubytes = T::unit(a.nb);  // boxes of columns this CTA loads
+    const uint32_t a_base = smem_u32(smem), p_base = a_base + a.units * ubytes;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + a.units * ubytes + T::SLOT_AREA);
+    const uint32_t bar0 = smem_u32(bars);
+    auto full = [&](int s) { return bar0 + 8u * s; };
+    auto empty = [&](int s) { return bar0 + 8u * (kDxMaxUnits + s); };
+    auto tfull = [&](int i) { return bar0 + 8u * (2 * kDxMaxUnits + i); };
+    auto tempty = [&](int i) { return bar0 + 8u * (2 * kDxMaxUnits + 2 + i); };
+    const uint32_t done = bar0 + 8u * (2 * kDxMaxUnits + 4);
+    const uint32_t addfull0 = bar0 + 8u * (2 * kDxMaxUnits + 5);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * kDxMaxUnits + 5 + EW * SLOTS);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = gg::cluster_rank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int mine = (a.tiles * a.slices - pair + pairs - 1) / pairs;
+    // tiles in token order over the pairs: rows of dx are written whole within a short time
+    auto pair_item = [&](int i, int &tile, int &slice) {
+        const int u = pair + i * pairs;  // tiles * slices is about N d / 65536
+        tile = u / a.slices;
+        slice = u - tile * a.slices;
+    };
+    auto item = [&](int i, int &tile, int &slice) {  // in tiles of 128 tokens
+        pair_item(i, tile, slice);
+        tile = 2 * tile + (int)rank;
+    };
+    const int chunks = (a.E + 31) / 32;
+    const int per_tile = BF16 ? chunks : chunks + (chunks + 2) / 3;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kDxMaxUnits; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(tfull(i), 1);
+            mbar_init(tempty(i), 2 * EW);
+        }
+        mbar_init(done, 1);
+        for (int i = 0; i < EW * SLOTS; ++i)
+            mbar_init(addfull0 + 8u * i, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        *abort_flag = 0;
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(tmem_slot)),
+                     "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    grid_go();
+    grid_wait();  // the planes of the kernel before
+    gg::tc_fence_before();
+    gg::cluster_sync_all();  // barriers initialised in both CTAs before any remote use
+    gg::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---------------- TMA (both CTAs)
+            int stage = 0;
+            uint32_t phase = 0, last[kDxMaxUnits];
+            bool issued[kDxMaxUnits];
+            for (int s = 0; s < kDxMaxUnits; ++s)
+                issued[s] = false;
+            bool ok = true;
+            for (int i = 0; i < mine && ok; ++i) {
+                int tile, slice;
+                pair_item(i, tile, slice);
+                const int t0 = tile * 256 + (int)rank * 128, cb = slice * a.nb + (int)rank * hb;
+                for (int u = 0; u < per_tile; ++u) {
+                    if (!gg::mbar_wait(empty(stage), phase ^ 1u, abort_flag, a.timeout_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t dst = a_base + stage * ubytes, wdst = dst + PLANES * 8192;
+                    const uint32_t bar = gg::map_to_rank(full(stage), 0);
+                    // chunks of the unit whose hi planes alone are wanted (fp32), or none
+                    const int c1 = 3 * (u - chunks);
+                    const int n1 = BF16 || u < chunks ? 0 : min(3, chunks - c1);
+                    if (rank == 0)
+                        mbar_arrive_expect_tx(full(stage),
+                                              2 * (n1 ? n1 * (8192 + hb * 4096) : ubytes));
+                    if (n1 == 0) {
+                        tma_load_3d_pair(dst, &tm_dl, 32 * u, t0, 0, bar);
+                        tma_load_4d_pair(wdst, &tm_w, 0, 32 * u, cb, 0, bar);
+                    } else {
+                        for (int p = 0; p < n1; ++p) {
+                            tma_load_3d_pair(dst + p * 8192, &tm_dl1, 32 * (c1 + p), t0, 0, bar);
+                            tma_load_4d_pair(wdst + p * hb * 4096, &tm_w1, 0, 32 * (c1 + p), cb, 0,
+                                             bar);
+                        }
+                    }
+                    issued[stage] = true;
+                    last[stage] = phase;
+                    if (++stage == a.units) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (rank == 0)  // its barriers count both CTAs' copies
+                for (int s = 0; s < a.units; ++s)
+                    if (issued[s])
+                        gg::mbar_wait(full(s), last[s], abort_flag, a.timeout_ns, false);
+        }
+    } else if (warp == 1) {
+        if (rank == 0 && elect_one()) {
+            // ---------------- MMA (first CTA of the pair)
+            const uint32_t id = idesc(256, 64 * a.nb, false, true);
+            int stage = 0, acc = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            bool ok = true;
+            for (int i = 0; i < mine && ok; ++i) {
+                if (!gg::mbar_wait(tempty(acc), acc_phase ^ 1u, abort_flag, a.timeout_ns))
+                    break;
+                gg::tc_fence_after();
+                const uint32_t d0 = tmem + (uint32_t)(acc * 256);
+                uint32_t accumulate = 0;
+                // one product: slot i of dl with slot j of the weights, ks steps of 16 experts (32
+                // bytes of a row of A, 2048 bytes of B)
+                for (int u = 0; u < per_tile; ++u) {
+                    if (!gg::mbar_wait(full(stage), phase, abort_flag, a.timeout_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    gg::tc_fence_after();
+                    const uint32_t at = a_base + stage * ubytes;
+                    auto product = [&](int x, int y, int ks) {
+                        const uint64_t ad = smem_desc_sw64(at + x * 8192);
+                        const uint64_t bd =
+                            smem_desc_mn_sw128(at + PLANES * 8192 + y * hb * 4096, 4096);
+                        gg::tc_mma_pair<0>(d0, ad, bd, id, accumulate);
+                        accumulate = 1;
+                        if (ks > 1)
+                            gg::tc_mma_pair<0>(d0, ad + 2, bd + 128, id, 1u);
+                    };
+                    if (BF16 || u < chunks) {
+                        const int ks = min(2, (a.E - 32 * u + 15) / 16);
+#pragma unroll
+                        for (int order = PLANES - 1; order >= (BF16 ? 0 : 1); --order)
+#pragma unroll
+                            for (int p = order; p >= 0; --p)
+                                product(p, order - p, ks);
+                    } else {
+                        const int c1 = 3 * (u - chunks), n1 = min(3, chunks - c1);
+                        for (int p = 0; p < n1; ++p)
+                            product(p, p, min(2, (a.E - 32 * (c1 + p) + 15) / 16));
+                    }
+                    gg::tc_commit_pair(gg::map_to_rank(empty(stage), 0));
+                    gg::tc_commit_pair(gg::map_to_rank(empty(stage), 1));
+                    if (++stage == a.units) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok)
+                    break;
+                gg::tc_commit_pair(gg::map_to_rank(tfull(acc), 0));
+                gg::tc_commit_pair(gg::map_to_rank(tfull(acc), 1));
+                acc ^= 1;
+                if (acc == 0)
+                    acc_phase ^= 1u;
+            }
+            gg::tc_commit_pair(gg::map_to_rank(done, 0));
+            gg::mbar_wait(done, 0, abort_flag, a.timeout_ns, false);
+        }
+    } else {
+        dx_epilogue<T, ADD>(a, tmem, p_base, mine, tm_dx, tm_add, tfull(0), addfull0, abort_flag,
+                            item, [&](int acc) {
+                                gg::mbar_arrive_cluster(gg::map_to_rank(tempty(acc), 0));
+                            });
+    }
+    __syncwarp();
+    gg::tc_fence_before();
+    if (*abort_flag) {
+        // after a timeout, give copies already in flight time to land before the pair leaves
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 2000000ull) {
+        }
+    }
+    gg::cluster_sync_all();  // neither CTA leaves while its partner may still use its memory
+    gg::tc_fence_after();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
                      : "memory");
 }
 
