@@ -8,9 +8,10 @@
 //   dloss/dl_te = p_te (cb E / M (f_e - sum_j f_j p_tj) + cz 2 / M lse_t)
 // (the counts are constants: no gradient passes through the selection).
 //
-// Both passes read the [N][E] logits once. A row is held by LPR lanes, 8 columns each, so the
-// softmax's maximum and sum are log2(LPR) shuffles and a lane owns the same columns in every
-// row it sees: the sums over tokens stay in its registers until the end of the block.
+// Both passes read the [N][E] logits once. A row is held by LPR lanes, up to 16 columns each, so
+// the softmax's maximum and sum are log2(LPR) shuffles and a lane owns the same columns in every
+// row it sees: the sums over tokens stay in its registers until the end of the block. Issue
+// slots bound the passes: with 8 columns a lane the shuffles were a third of the instructions.
 #pragma once
 
 #include "common.cuh"
@@ -18,22 +19,21 @@
 namespace moe {
 
 constexpr int kBalThreads = 1024;
-constexpr int kBalCols = 8;  // columns of a row held by one lane
-constexpr int kRows = 2;     // rows a lane group takes at once
 
-// Lane l of the LPR lanes of a row holds columns col(j), j = 0..7: two 16-byte chunks (VEC,
-// E % 4 == 0) or 8 columns LPR apart. A column at or past E reads as -inf (probability 0).
-template <int LPR, bool VEC>
+// Lane l of the LPR lanes of a row holds C = 4 NC columns col(j): NC 16-byte chunks (VEC,
+// E % 4 == 0) or C columns LPR apart. A column at or past E reads as -inf (probability 0).
+template <int LPR, int NC, bool VEC>
 struct RowSlice {
+    static constexpr int C = 4 * NC;
     static __device__ __forceinline__ int col(int l, int j)
     {
         return VEC ? 4 * (l + LPR * (j / 4)) + (j & 3) : l + LPR * j;
     }
-    static __device__ __forceinline__ void load(const float *row, int E, int l, float (&v)[8])
+    static __device__ __forceinline__ void load(const float *row, int E, int l, float (&v)[C])
     {
         if constexpr (VEC) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < NC; ++i) {
                 const int c = 4 * (l + LPR * i);
                 const float4 q = c < E ? *reinterpret_cast<const float4 *>(row + c)
                                        : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
@@ -44,17 +44,17 @@ struct RowSlice {
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < C; ++j) {
                 const int c = l + LPR * j;
                 v[j] = c < E ? row[c] : -INFINITY;
             }
         }
     }
-    static __device__ __forceinline__ void store(float *row, int E, int l, const float (&v)[8])
+    static __device__ __forceinline__ void store(float *row, int E, int l, const float (&v)[C])
     {
         if constexpr (VEC) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < NC; ++i) {
                 const int c = 4 * (l + LPR * i);
                 if (c < E)
                     *reinterpret_cast<float4 *>(row + c) =
@@ -62,7 +62,7 @@ struct RowSlice {
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < C; ++j) {
                 const int c = l + LPR * j;
                 if (c < E)
                     row[c] = v[j];
@@ -92,19 +92,19 @@ __device__ __forceinline__ float row_sum(float v)
 // by their sum. Returns the sum; lse: the log-sum-exp. With L = log2(e), e^(v - m) is
 // 2^(v L - m L), one fused multiply-add: the rounding of m L is common to the row and cancels in
 // the probabilities. Results below fp32's normal range are 0.
-template <int LPR>
-__device__ __forceinline__ float row_softmax(float (&v)[8], float &lse)
+template <int LPR, int C>
+__device__ __forceinline__ float row_softmax(float (&v)[C], float &lse)
 {
     constexpr float kL = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
     float m = v[0];
 #pragma unroll
-    for (int j = 1; j < 8; ++j)
+    for (int j = 1; j < C; ++j)
         m = fmaxf(m, v[j]);
     m = row_max<LPR>(m);
     const float c = -m * kL;
     float s = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < C; ++j) {
         asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(v[j]) : "f"(fmaf(v[j], kL, c)));
         s += v[j];
     }
@@ -161,17 +161,18 @@ __device__ __forceinline__ void balance_outputs(const BalanceOut &o, double prob
     }
 }
 
-// Sums over this block's tokens. SINGLE: the grid is one block, which also writes the outputs.
-template <int LPR, bool VEC, bool SINGLE>
+// Sums over this block's tokens. A grid of one block also writes the outputs.
+template <int LPR, int NC, bool VEC>
 __global__ void __launch_bounds__(kBalThreads, 1)
     balance_sums_kernel(const float *__restrict__ logits, const int32_t *__restrict__ topk_idx,
                         const uint8_t *__restrict__ mask, int N, BalanceParts parts,
                         BalanceOut out)
 {
-    using Slice = RowSlice<LPR, VEC>;
+    using Slice = RowSlice<LPR, NC, VEC>;
+    constexpr int C = Slice::C;
     constexpr int GW = 32 / LPR;  // rows of a warp at once
     constexpr int WARPS = kBalThreads / 32;
-    __shared__ float s_prob[WARPS * LPR * kBalCols];  // 32 warps x up to 256 columns
+    __shared__ float s_prob[WARPS * LPR * C];  // up to 256 columns a warp
     __shared__ int s_count[256];
     __shared__ float s_z[WARPS];
     __shared__ int s_m[WARPS];
@@ -184,57 +185,39 @@ __global__ void __launch_bounds__(kBalThreads, 1)
         s_count[tid] = 0;
     __syncthreads();
 
-    // kRows rows of a lane group at once: their loads are in flight together, and their shuffles
-    // fill each other's latency
-    float acc[8] = {};
+    float acc[C] = {};
     float zsum = 0.0f;
     int m_tok = 0;
     bool bad_index = false, bad_logit = false;
-    const int64_t stride = (int64_t)gridDim.x * WARPS * GW * kRows;
-    for (int64_t base = ((int64_t)blockIdx.x * WARPS + warp) * GW * kRows; base < N;
-         base += stride) {
-        float v[kRows][8];
-        bool live[kRows];
-#pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-            const int64_t t = base + r * GW + grp;
-            live[r] = t < N && (!mask || mask[t]);
-            Slice::load(logits + (t < N ? t : 0) * E, t < N ? E : 0, l, v[r]);
-        }
-        // counts: lane l takes the slots l, l + LPR, ... of its tokens
+    const int64_t stride = (int64_t)gridDim.x * WARPS * GW;
+    for (int64_t base = ((int64_t)blockIdx.x * WARPS + warp) * GW; base < N; base += stride) {
+        const int64_t t = base + grp;
+        const bool inside = t < N, live = inside && (!mask || mask[t]);
+        float v[C];
+        Slice::load(logits + (inside ? t : 0) * E, inside ? E : 0, l, v);
+        // counts: lane l takes the slots l, l + LPR, ... of its token
         for (int k = l; k < K; k += LPR) {
-            int e[kRows];
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                const int64_t t = base + r * GW + grp;
-                e[r] = t < N ? topk_idx[t * K + k] : 0;
-            }
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                const bool ok = (unsigned)e[r] < (unsigned)E;
-                if (live[r] && ok)
-                    atomicAdd(&s_count[e[r]], 1);
-                bad_index |= live[r] && !ok;
-            }
+            const int e = inside ? topk_idx[t * K + k] : 0;
+            const bool ok = (unsigned)e < (unsigned)E;
+            if (live && ok)
+                atomicAdd(&s_count[e], 1);
+            bad_index |= live && !ok;
         }
+        if (!live) {  // keeps the arithmetic of a row left out finite
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-            if (!live[r]) {  // keeps the arithmetic of a row left out finite
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    v[r][j] = 0.0f;
-            }
-            float lse;
-            const float s = row_softmax<LPR>(v[r], lse);
-            const float inv = live[r] ? __fdividef(1.0f, s) : 0.0f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                acc[j] = fmaf(v[r][j], inv, acc[j]);
-            lse = live[r] ? lse : 0.0f;
-            bad_logit |= !isfinite(lse);
-            zsum = fmaf(lse, lse, zsum);
-            m_tok += live[r];
+            for (int j = 0; j < C; ++j)
+                v[j] = 0.0f;
         }
+        float lse;
+        const float s = row_softmax<LPR>(v, lse);
+        const float inv = live ? __fdividef(1.0f, s) : 0.0f;
+#pragma unroll
+        for (int j = 0; j < C; ++j)
+            acc[j] = fmaf(v[j], inv, acc[j]);
+        lse = live ? lse : 0.0f;
+        bad_logit |= !isfinite(lse);
+        zsum = fmaf(lse, lse, zsum);
+        m_tok += live;
     }
     if (bad_index)
         set_dev_error(MOE_ERR_DEVICE_BOUNDS);
@@ -249,13 +232,13 @@ __global__ void __launch_bounds__(kBalThreads, 1)
 #pragma unroll
     for (int off = LPR; off < 32; off <<= 1) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < C; ++j)
             acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], off);
     }
     if (grp == 0) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            s_prob[warp * (LPR * kBalCols) + Slice::col(l, j)] = acc[j];
+        for (int j = 0; j < C; ++j)
+            s_prob[warp * (LPR * C) + Slice::col(l, j)] = acc[j];
     }
     zsum = warp_sum(zsum);
     m_tok = warp_sum(m_tok);
@@ -268,17 +251,17 @@ __global__ void __launch_bounds__(kBalThreads, 1)
     if (tid < E) {
 #pragma unroll 8
         for (int w = 0; w < WARPS; ++w)
-            p += s_prob[w * (LPR * kBalCols) + tid];
+            p += s_prob[w * (LPR * C) + tid];
     }
     float z = 0.0f;
     int mt = 0;
-    if (tid == 0 || SINGLE) {
+    if (tid == 0 || gridDim.x == 1) {
         for (int w = 0; w < WARPS; ++w) {
             z += s_z[w];
             mt += s_m[w];
         }
     }
-    if constexpr (SINGLE) {
+    if (gridDim.x == 1) {
         balance_outputs(out, p, tid < E ? s_count[tid] : 0, z, mt, s_red);
     } else {
         if (tid < E) {
@@ -356,61 +339,54 @@ __global__ void __cluster_dims__(kFinishBlocks, 1, 1) __launch_bounds__(1024, 1)
 }
 
 // dlogits from the logits, the counts and the number of counted tokens.
-template <int LPR, bool VEC>
+template <int LPR, int NC, bool VEC>
 __global__ void __launch_bounds__(256)
     balance_grad_kernel(const float *logits, const uint8_t *__restrict__ mask,
                         const int32_t *__restrict__ counts, const int32_t *__restrict__ tokens,
                         const float *__restrict__ dloss, int N, int E, int K, float cb, float cz,
                         float *dlogits)
 {
-    using Slice = RowSlice<LPR, VEC>;
+    using Slice = RowSlice<LPR, NC, VEC>;
+    constexpr int C = Slice::C;
     constexpr int GW = 32 / LPR;
     const int warp = (blockIdx.x * 256 + threadIdx.x) >> 5, lane = threadIdx.x & 31;
     const int l = lane % LPR, grp = lane / LPR;
     const int M = tokens[0];
-    const float inv_m = M > 0 ? 1.0f / (float)M : 0.0f;
+    const float inv_m = M > 0 ? 1.0f / (float)M : 0.0f, inv_mk = inv_m / (float)K;
     const float scale = (dloss ? dloss[0] : 1.0f) * inv_m;
     const float a = scale * cb * (float)E, b = scale * cz * 2.0f;
-    float f[8];
+    float f[C];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < C; ++j) {
         const int c = Slice::col(l, j);
-        f[j] = c < E ? (float)counts[c] * inv_m / (float)K : 0.0f;
+        f[j] = c < E ? (float)counts[c] * inv_mk : 0.0f;
     }
-    const int64_t stride = (int64_t)(gridDim.x * 256 / 32) * GW * kRows;
-    for (int64_t base = (int64_t)warp * GW * kRows; base < N; base += stride) {
-        float v[kRows][8];
-        bool live[kRows];
+    const int64_t stride = (int64_t)(gridDim.x * 256 / 32) * GW;
+    for (int64_t base = (int64_t)warp * GW; base < N; base += stride) {
+        const int64_t t = base + grp;
+        const bool inside = t < N, live = inside && (!mask || mask[t]);
+        float v[C];
+        Slice::load(logits + (inside ? t : 0) * E, inside ? E : 0, l, v);
+        if (!live) {
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-            const int64_t t = base + r * GW + grp;
-            live[r] = t < N && (!mask || mask[t]);
-            Slice::load(logits + (t < N ? t : 0) * E, t < N ? E : 0, l, v[r]);
+            for (int j = 0; j < C; ++j)
+                v[j] = 0.0f;
         }
+        float lse;
+        const float s = row_softmax<LPR>(v, lse);
+        float dot = 0.0f;
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-            const int64_t t = base + r * GW + grp;
-            if (!live[r]) {
+        for (int j = 0; j < C; ++j)
+            dot += f[j] * v[j];
+        dot = row_sum<LPR>(dot);
+        const float inv = __fdividef(1.0f, s);
+        // p (a (f - inner) + b lse) = e (a f + c) / sum
+        const float c = b * lse - a * dot * inv;
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    v[r][j] = 0.0f;
-            }
-            float lse;
-            const float s = row_softmax<LPR>(v[r], lse);
-            float dot = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                dot += f[j] * v[r][j];
-            dot = row_sum<LPR>(dot);
-            const float inv = __fdividef(1.0f, s);
-            // p (a (f - inner) + b lse) = e (a f + c) / sum
-            const float c = b * lse - a * dot * inv;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[r][j] = live[r] ? v[r][j] * inv * (a * f[j] + c) : 0.0f;
-            if (t < N)
-                Slice::store(dlogits + t * E, E, l, v[r]);
-        }
+        for (int j = 0; j < C; ++j)
+            v[j] = live ? v[j] * inv * (a * f[j] + c) : 0.0f;
+        if (inside)
+            Slice::store(dlogits + t * E, E, l, v);
     }
 }
 

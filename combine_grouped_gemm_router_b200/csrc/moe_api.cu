@@ -1166,7 +1166,7 @@ moe_status_t combine_impl(const moe_shape_t *s, const void *y, const int32_t *ro
 
 // Blocks of the balance sums: one per SM, and no more than give each warp a row. One block
 // takes a small call alone (and writes its outputs, without a second kernel).
-constexpr int64_t kBalSingle = 32768;  // logits of a call that one block takes
+constexpr int64_t kBalSingle = 8192;  // logits of a call that one block takes
 
 int balance_blocks(const moe_shape_t *s)
 {
@@ -1197,29 +1197,47 @@ BalanceLayout balance_layout(const moe_shape_t *s)
     return L;
 }
 
-// go(lanes per row, vector loads) as compile-time constants.
+// go(lanes of a row) as a compile-time constant: as many lanes of 8 columns as E needs.
+template <typename F>
+void row_lanes(int E, F &&go)
+{
+    using std::integral_constant;
+    if (E <= 8)
+        go(integral_constant<int, 1>{});
+    else if (E <= 16)
+        go(integral_constant<int, 2>{});
+    else if (E <= 32)
+        go(integral_constant<int, 4>{});
+    else if (E <= 64)
+        go(integral_constant<int, 8>{});
+    else if (E <= 128)
+        go(integral_constant<int, 16>{});
+    else
+        go(integral_constant<int, 32>{});
+}
+
+// go(lanes of a row, chunks of 4 columns a lane, vector loads) for the balance kernels. 8 columns
+// a lane up to 128 experts; above, 16 lanes of 12 or 16 columns, two rows of a warp at once (measured
+// against 8 columns: 131072 x 256 35.7 -> 32.7 us, but 32768 x 64 7.5 -> 8.4 with 16).
 template <typename F>
 void row_slices(int E, F &&go)
 {
-    auto lanes = [&](auto vec) {
-        using std::integral_constant;
-        if (E <= 8)
-            go(integral_constant<int, 1>{}, vec);
-        else if (E <= 16)
-            go(integral_constant<int, 2>{}, vec);
-        else if (E <= 32)
-            go(integral_constant<int, 4>{}, vec);
-        else if (E <= 64)
-            go(integral_constant<int, 8>{}, vec);
-        else if (E <= 128)
-            go(integral_constant<int, 16>{}, vec);
+    using std::integral_constant;
+    auto with = [&](auto lanes, auto chunks) {
+        if (E % 4 == 0)
+            go(lanes, chunks, std::true_type{});
         else
-            go(integral_constant<int, 32>{}, vec);
+            go(lanes, chunks, std::false_type{});
     };
-    if (E % 4 == 0)
-        lanes(std::true_type{});
+    if (E > 192)
+        with(integral_constant<int, 16>{}, integral_constant<int, 4>{});
+    else if (E > 128)
+        with(integral_constant<int, 16>{}, integral_constant<int, 3>{});
     else
-        lanes(std::false_type{});
+        row_lanes(E, [&](auto lanes) {
+            if constexpr (decltype(lanes)::value <= 16)
+                with(lanes, integral_constant<int, 2>{});
+        });
 }
 
 moe_status_t balance_loss_impl(const moe_shape_t *s, const float *logits, const int32_t *topk_idx,
@@ -1233,15 +1251,9 @@ moe_status_t balance_loss_impl(const moe_shape_t *s, const float *logits, const 
     int blocks = balance_blocks(s);
     if (blocks > kBalMaxBlocks)
         blocks = kBalMaxBlocks;
-    row_slices(s->E, [&](auto lpr, auto vec) {
-        constexpr int LPR = decltype(lpr)::value;
-        constexpr bool VEC = decltype(vec)::value;
-        if (blocks == 1)
-            balance_sums_kernel<LPR, VEC, true>
-                <<<1, kBalThreads, 0, st>>>(logits, topk_idx, mask, s->N, parts, out);
-        else
-            balance_sums_kernel<LPR, VEC, false>
-                <<<blocks, kBalThreads, 0, st>>>(logits, topk_idx, mask, s->N, parts, out);
+    row_slices(s->E, [&](auto lpr, auto nc, auto vec) {
+        balance_sums_kernel<decltype(lpr)::value, decltype(nc)::value, decltype(vec)::value>
+            <<<blocks, kBalThreads, 0, st>>>(logits, topk_idx, mask, s->N, parts, out);
     });
     if (blocks > 1)
         if (launch_chained(balance_finish_kernel, kFinishBlocks, 1024, 0, st, 1, parts, blocks, out) !=
@@ -1254,14 +1266,14 @@ moe_status_t balance_grad_impl(const moe_shape_t *s, const float *logits, const 
                                const int32_t *counts, const int32_t *tokens, const float *dloss,
                                float cb, float cz, float *dlogits, cudaStream_t st)
 {
-    row_slices(s->E, [&](auto lpr, auto vec) {
+    row_slices(s->E, [&](auto lpr, auto nc, auto vec) {
         constexpr int LPR = decltype(lpr)::value;
-        constexpr bool VEC = decltype(vec)::value;
-        const int64_t rows_per_block = 8 * (32 / LPR) * kRows;
+        const int64_t rows_per_block = 8 * (32 / LPR);
         const int64_t want = (s->N + rows_per_block - 1) / rows_per_block;
-        const int64_t most = 8 * (int64_t)num_sms();
-        balance_grad_kernel<LPR, VEC><<<(int)(want < most ? want : most), 256, 0, st>>>(
-            logits, mask, counts, tokens, dloss, s->N, s->E, s->K, cb, cz, dlogits);
+        const int64_t most = 4 * (int64_t)num_sms();  // a thread's share of the counts pays for itself
+        balance_grad_kernel<LPR, decltype(nc)::value, decltype(vec)::value>
+            <<<(int)(want < most ? want : most), 256, 0, st>>>(
+                logits, mask, counts, tokens, dloss, s->N, s->E, s->K, cb, cz, dlogits);
     });
     return launch_status();
 }
@@ -1462,7 +1474,7 @@ moe_status_t route_backward_impl(const moe_shape_t *s, const RouteBackward &a, c
                                s->d, (s->flags & MOE_FLAG_OUT_BF16) ? 1 : 0};
         const int blocks = (s->d + rb::kSmallCols - 1) / rb::kSmallCols;
         moe_status_t rc = MOE_OK;
-        row_slices(s->E, [&](auto lpr, auto) {
+        row_lanes(s->E, [&](auto lpr) {
             auto kern = rb::router_small_grad_kernel<decltype(lpr)::value>;
             if (smem_attr_once(kern, rb::kSmallSmem) != cudaSuccess)
                 rc = MOE_ERR_CUDA;
@@ -1483,7 +1495,7 @@ moe_status_t route_backward_impl(const moe_shape_t *s, const RouteBackward &a, c
         const int64_t want = ((int64_t)s->E * s->d / 8 + rb::kSplitThreads - 1) / rb::kSplitThreads;
         w_blocks = (int)(want < num_sms() ? want : num_sms());
     }
-    row_slices(s->E, [&](auto lpr, auto) {
+    row_lanes(s->E, [&](auto lpr) {
         rb::router_split_grad_kernel<decltype(lpr)::value>
             <<<sa.token_blocks + w_blocks, rb::kSplitThreads, 0, st>>>(sa);
     });
