@@ -2120,6 +2120,14 @@ moe_route_backward(const moe_shape_t *shape, const uint16_t *x, const float *w_r
     if ((!dtopk_w && !dlogits) || (dtopk_w && (!topk_idx || !topk_w)) || (dx && !w_router) ||
         (dw_router && !x))
         return MOE_ERR_INVALID_ARG;
+    if (shape->N > 1 << 30)
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    // dx is written before x is read for dWr
+    const size_t nd = (size_t)shape->N * shape->d;
+    const char *x0 = reinterpret_cast<const char *>(x), *dx0 = static_cast<const char *>(dx);
+    if (dx && dw_router && x0 < dx0 + nd * ((shape->flags & MOE_FLAG_OUT_BF16) ? 2 : 4) &&
+        dx0 < x0 + nd * 2)
+        return MOE_ERR_INVALID_ARG;
     if ((x && !aligned16(x)) || (w_router && !aligned16(w_router)) ||
         (topk_idx && !aligned4(topk_idx)) || (topk_w && !aligned4(topk_w)) ||
         (dtopk_w && !aligned4(dtopk_w)) || (dlogits && !aligned16(dlogits)) ||

@@ -574,7 +574,12 @@ size_t moe_route_backward_workspace_size(const moe_shape_t *shape);
  * dx [N][d] fp32, or bf16 with MOE_FLAG_OUT_BF16; dx_add [N][d] bf16, nullable (the gradient
  * that reaches x by other ways; a bf16 dx may alias it); a masked token's dx is dx_add or 0.
  * dw_router [E][d], dbias [E] fp32. Each of dx (with w_router), dw_router (with x) and dbias
- * may be NULL, not all three. N = 0 writes zero weight gradients.
+ * may be NULL, not all three; dx may not overlap x (MOE_ERR_INVALID_ARG). N = 0 writes zero
+ * weight gradients. N <= 2^30.
+ * Precision: dl and the fp32 outputs as fp32 sums (the tensor cores run on bf16 terms of the
+ * fp32 factors, three of each: nothing of dl is lost); a bf16 dx to 2^-14 before its own
+ * rounding. The same bits every run. A non-finite gradient, weight or (unmasked) hidden state
+ * gives non-finite results where it enters; an infinity may arrive as NaN.
  * ws as for moe_balance_loss, moe_route_backward_workspace_size bytes. */
 moe_status_t moe_route_backward(const moe_shape_t *shape, const uint16_t *x,
                                 const float *w_router, const int32_t *topk_idx,

@@ -91,7 +91,10 @@ def check(a, E, out, bf16=False, gate=True, loss=True, add=False):
 SHAPES = [(1, 8, 1, 1), (1, 128, 256, 8), (2, 24, 3, 2), (63, 136, 8, 2), (64, 128, 8, 2),
           (65, 64, 64, 6), (127, 120, 65, 4), (128, 256, 128, 8), (129, 264, 96, 32),
           (300, 72, 17, 5), (513, 512, 200, 8), (1111, 1000, 64, 6), (2049, 384, 130, 3),
-          (700, 2048, 256, 8), (4097, 128, 40, 2)]
+          (700, 2048, 256, 8), (4097, 128, 40, 2),
+          # the tensor-core path on narrow and ragged x, on E just past 64 and 128
+          (260, 8, 3, 2), (1000, 24, 100, 4), (258, 40, 65, 1), (385, 200, 129, 3),
+          (2000, 328, 64, 1), (515, 1032, 33, 32)]
 
 
 @pytest.mark.parametrize("bf16", [False, True])
@@ -225,3 +228,49 @@ def test_repeats_streams_and_graphs(E, bf16):
                              dlogits=g["dlogits"], token_mask=g["mask"], dx_add=over, ws=out["ws"])
         assert torch.equal(over, first["dx"])
     assert m.moe_get_device_error(True) == 0
+
+
+def test_dx_over_x_is_refused():
+    m = lib()
+    shape = m.make_shape(300, 64, 128, 8, 2, 1, out_bf16=True)
+    x = torch.zeros(300, 64, dtype=torch.bfloat16, device="cuda")
+    wr = torch.zeros(8, 64, device="cuda")
+    dl = torch.zeros(300, 8, device="cuda")
+    ws = torch.empty(m.moe_route_backward_workspace_size(shape), dtype=torch.uint8, device="cuda")
+    with pytest.raises(m.MoeError, match="INVALID_ARG"):
+        m.moe_route_backward(shape, x, wr, x, torch.zeros_like(wr), dlogits=dl, ws=ws)
+    m.moe_route_backward(shape, x, wr, x, None, dlogits=dl, ws=ws)   # x is not read then
+
+
+FIRST_CALL = """
+import torch, combine_grouped_gemm_router_b200 as m
+N, d, E, K = 700, 256, {E}, 2
+sh = m.make_shape(N, d, 128, E, K, 1)
+z = lambda *s, **k: torch.zeros(*s, device="cuda", **k)
+x, wr, dl = torch.ones(N, d, device="cuda", dtype=torch.bfloat16), z(E, d), torch.ones(N, E, device="cuda")
+idx, counts, tok = z(N, K, dtype=torch.int32), z(E, dtype=torch.int32), z(1, dtype=torch.int32)
+dx, dw, db, loss, mean = z(N, d), z(E, d), z(E), z(3), z(E)
+ws = torch.empty(m.moe_route_backward_workspace_size(sh) + m.moe_balance_workspace_size(sh),
+                 dtype=torch.uint8, device="cuda")
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    m.moe_balance_loss(sh, dl, idx, loss, counts, mean, tok, ws=ws)
+    m.moe_route_backward(sh, x, wr, dx, dw, dbias=db, dlogits=dl, ws=ws)
+g.replay()
+torch.cuda.synchronize()
+assert torch.all(dw == N) and torch.all(db == N) and tok.item() == N and counts[0].item() == N * K
+print("ok")
+"""
+
+
+@pytest.mark.parametrize("E", [16, 200])
+def test_first_call_of_a_process_may_be_captured(E):
+    """The one-time setup of the kernels (shared-memory limits, resident pairs) does not need an
+    eager call before a capture."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL.format(E=E)], cwd=root, timeout=120,
+                       capture_output=True, text=True)
+    assert r.returncode == 0 and "ok" in r.stdout, r.stderr[-800:]

@@ -71,7 +71,8 @@ def test_route_backward_refusals(m):
     assert need > 0 and m.moe_route_backward_workspace_size(m.make_shape(3, 12, 0, 8, 2, 1)) == 0
     f = m._lib.moe_route_backward
     # shape, x, w_router, topk_idx, topk_w, dtopk_w, dlogits, mask, dx_add, dx, dw, dbias, ws, bytes
-    ok = [s, P, P, P, P, P, P, None, None, P, P, P, P, need, None]
+    Q = P + (1 << 24)
+    ok = [s, P, P, P, P, P, P, None, None, Q, P, P, P, need, None]
 
     def status(*at):
         args = list(ok)
@@ -84,12 +85,14 @@ def test_route_backward_refusals(m):
     assert status((2, None)) == 1                            # dx without the weights
     assert status((9, None), (10, None), (11, None)) == 1    # nothing wanted
     for i in (1, 2, 6, 8, 9, 10):
-        assert status((i, P + 4)) == 4, i
+        assert status((i, Q + 4 if i == 9 else P + 4)) == 4, i
+    assert status((9, P)) == 1 and status((9, P + 64 * 128 * 2 - 16)) == 1   # dx over x
     for i in (3, 4, 5, 11):
         assert status((i, P + 2)) == 4, i
     assert status((12, None)) == 3 and status((13, need - 1)) == 3 and status((12, P + 8)) == 4
     assert status((0, ctypes.byref(m.make_shape(64, 100, 256, 8, 2, 4)))) == 2   # d % 8
     assert status((0, ctypes.byref(m.make_shape(64, 128, 256, 8, 33, 4)))) == 1
+    assert status((0, ctypes.byref(m.make_shape((1 << 30) + 4, 128, 256, 8, 1, 4)))) == 2
 
 
 def test_checkpoint_refusals(m):
