@@ -338,10 +338,10 @@ template <bool FOLD>
 struct DwTile {
     static constexpr int NE = FOLD ? 1 : 2;     // boxes of 64 experts
     static constexpr int XB = 4;                // boxes of 64 columns of x
-    // tokens of a shared-memory stage. 64; 32 where two stages of 64 are all that fits (57 -> 48
-    // us at 16384 x 4096 x 128), though not where the zeroing of masked rows is what a stage
-    // waits for (FOLD: 64 against 80 us with a mask at 32768 x 4096 x 64)
-    static constexpr int TOK = FOLD ? 64 : 32;
+    // Tokens of a shared-memory stage. With 64, two (FOLD: three) stages fit, and a stage that
+    // waits for its masked rows is missed: 64 -> 58 us with a mask at 32768 x 4096 x 64, 57 ->
+    // 46 us at 16384 x 4096 x 128.
+    static constexpr int TOK = 32;
     static constexpr int BOX = TOK * 128;       // a box of them: 64 columns
     static constexpr int STAGE = (XB + 3 * NE) * BOX;
     static constexpr int ZERO = FOLD ? BOX : 0;
@@ -362,8 +362,8 @@ struct DwArgs {
     uint64_t timeout_ns;
 };
 
-// Warps: 0 TMA, 1 MMA, 2 zeroes the rows of x of masked tokens (a masked row may hold NaN, and
-// 0 * NaN would reach every sum), 4..11 the running sums.
+// Warps: 0 TMA, 1 MMA, 2 and 3 zero the rows of x of masked tokens (a masked row may hold NaN,
+// and 0 * NaN would reach every sum), 4..11 the running sums.
 template <bool FOLD>
 __global__ void __launch_bounds__(kDwThreads, 1)
     router_dw_kernel(const __grid_constant__ CUtensorMap tm_x,
@@ -524,12 +524,10 @@ __global__ void __launch_bounds__(kDwThreads, 1)
             gg::tc_commit(done);
             gg::mbar_wait(done, 0, abort_flag, a.timeout_ns, false);
         }
-    } else if (warp == 2) {
+    } else if (warp < 4) {
         if (a.mask) {
-            int stage = 0;
-            uint32_t phase = 0;
-            int ok = 1;
-            // the mask bytes of the next stage's tokens are loaded while this one is awaited
+            // two warps, every other stage each; the mask bytes of a warp's next stage are loaded
+            // while this one is awaited
             const int64_t t_end = min((int64_t)c1 * kChunk, (int64_t)a.N);
             auto masked = [&](int64_t t0) {  // bit i: token t0 + 32 i + lane
                 uint32_t m = 0;
@@ -539,12 +537,16 @@ __global__ void __launch_bounds__(kDwThreads, 1)
                         m |= (uint32_t)(a.mask[t0 + 32 * i + lane] == 0) << i;
                 return m;
             };
-            uint32_t next = masked((int64_t)c0 * kChunk);
-            for (int64_t t0 = (int64_t)c0 * kChunk; t0 < t_end; t0 += TOK) {
+            int ok = 1;
+            int64_t t0 = (int64_t)c0 * kChunk + (warp - 2) * TOK;
+            uint32_t next = masked(t0);
+            for (int n = warp - 2; t0 < t_end; n += 2, t0 += 2 * TOK) {
+                const int stage = n % S;
                 const uint32_t now = next;
-                next = masked(t0 + TOK);
+                next = masked(t0 + 2 * TOK);
                 if (lane == 0)
-                    ok = gg::mbar_wait(full(stage), phase, abort_flag, a.timeout_ns) ? 1 : 0;
+                    ok = gg::mbar_wait(full(stage), (uint32_t)(n / S) & 1u, abort_flag,
+                                       a.timeout_ns) ? 1 : 0;
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok)
                     break;
@@ -567,10 +569,6 @@ __global__ void __launch_bounds__(kDwThreads, 1)
                 }
                 if (lane == 0)
                     mbar_arrive(clean(stage));
-                if (++stage == S) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
             }
         }
     } else if (warp >= 4) {
