@@ -24,7 +24,8 @@ __host__ __device__ constexpr int checkpoint_stride(int f)
 // A block covers TY rows at once and TX chunks of 8 columns of each (16 bytes of every bf16 row: a
 // warp's accesses are whole lines; 16 columns a thread wrote half sectors and took 774 us where
 // this takes 519, 196608 rows of 1536); TX = 1 << tx_log2 divides f / 8. kActItems items of a
-// thread are loaded before the first is worked on (1: 611 us, 2: 519, 4: 614). Bound by
+// thread are loaded before the first is worked on (1: 611 us, 2: 519, 4: 614). With few rows the
+// columns are shared out too (gridDim.y). Bound by
 // memory: 3.04 GB in 519 us, 0.89 of the measured copy rate.
 constexpr int kActItems = 2;
 
@@ -36,13 +37,15 @@ __global__ void __launch_bounds__(256)
 {
     const int rows = max(0, min(*rows_dev, rows_alloc));
     const int tx = threadIdx.x & ((1 << tx_log2) - 1), ty = threadIdx.x >> tx_log2;
-    const int TX = 1 << tx_log2, TY = 256 >> tx_log2, chunks = f / 8, stride = checkpoint_stride(f);
-    const int per_row = chunks >> tx_log2;  // chunks of a thread in a row
+    const int TX = 1 << tx_log2, TY = 256 >> tx_log2, stride = checkpoint_stride(f);
+    const int groups = (f / 8) >> tx_log2;  // groups of TX chunks of a row, and this block's
+    const int g0 = groups * blockIdx.y / gridDim.y, g1 = groups * (blockIdx.y + 1) / gridDim.y;
+    const int per_row = g1 - g0, first = (g0 << tx_log2) + tx, end = g1 << tx_log2;
     // item i of this thread: chunk i % per_row of its row i / per_row
     const int64_t r0 = (int64_t)blockIdx.x * TY + ty, step = (int64_t)gridDim.x * TY;
     const int64_t items = r0 < rows ? ((rows - r0 + step - 1) / step) * per_row : 0;
     int64_t r = r0;
-    int c = tx;
+    int c = first;
     for (int64_t i = 0; i < items; i += kActItems) {
         uint2 gc[kActItems], uc[kActItems];
         uint4 dq[kActItems];
@@ -59,8 +62,8 @@ __global__ void __launch_bounds__(256)
                 gs[k] = pow2f((int)row[2 * f + c / 4] - 127);
                 us[k] = pow2f((int)row[2 * f + f / 32 + c / 4] - 127);
                 c += TX;
-                if (c >= chunks) {
-                    c = tx;
+                if (c >= end) {
+                    c = first;
                     r += step;
                 }
             }

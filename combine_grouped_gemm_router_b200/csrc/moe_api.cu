@@ -1326,12 +1326,28 @@ int split_blocks(const moe_shape_t *s)
 // a multiple of 16 bytes.
 int dl_pitch_of(const moe_shape_t *s) { return s->E > 64 ? (s->E + 63) & ~63 : (s->E + 7) & ~7; }
 
+// Shares of the token tiles of the little-work path: with one tile there are no partial results and
+// one launch does it all, else two blocks to an SM.
+int block_parts(const moe_shape_t *s)
+{
+    const int tiles = (s->N + 63) / 64, cols = (s->d + 63) / 64;
+    const int want = 2 * num_sms() / cols;
+    return want < 1 ? 1 : want < tiles ? want : tiles;
+}
+
 RouteBackLayout route_back_layout(const moe_shape_t *s)
 {
     RouteBackLayout L;
     const size_t pitch = dl_pitch_of(s);
     const DwGeometry g = dw_geometry(s);
     size_t o = 0;
+    if (rb::block_path(s->N, s->E, s->d)) {
+        const size_t parts = (size_t)block_parts(s);
+        L.dl = L.wp = L.bias = 0;
+        L.part = align_up(parts * s->E * 4);
+        L.total = L.part + align_up(parts * s->E * s->d * 4);
+        return L;
+    }
     L.dl = o;
     o = align_up(o + 3 * (size_t)s->N * pitch * 2);
     L.wp = o;
@@ -1465,23 +1481,53 @@ moe_status_t launch_router_dw(const moe_shape_t *s, const DwGeometry &g, const u
     return s->E <= 64 ? go(std::true_type{}) : go(std::false_type{});
 }
 
+// Not chained: its blocks, scheduled early beside dWr's, cost more than the launch they hide (128
+// experts, 8192 x 2048: 52 against 48 us in all).
+moe_status_t launch_router_sum(rb::SumArgs &a, cudaStream_t st)
+{
+    const int64_t groups = a.dw ? (int64_t)a.E * a.d / 4 : 0;
+    const bool few = groups <= 16384;
+    a.dw_blocks = (int)(few ? (groups + 31) / 32 : (groups + 255) / 256);
+    const int blocks = a.dw_blocks + (a.dbias ? (a.E + 7) / 8 : 0);
+    if (few)
+        rb::router_sum_kernel<8><<<blocks, 256, 0, st>>>(a);
+    else
+        rb::router_sum_kernel<1><<<blocks, 256, 0, st>>>(a);
+    return launch_status();
+}
+
 moe_status_t route_backward_impl(const moe_shape_t *s, const RouteBackward &a, char *ws,
                                  cudaStream_t st)
 {
     const rb::GradIn in{a.topk_idx, a.topk_w, a.dtopk_w, a.dlogits, a.mask};
-    if (s->N <= rb::kSmallTokens && (int64_t)s->N * s->E <= rb::kSmallLogits) {
-        const rb::SmallArgs sm{in, a.x, a.w_router, a.dx_add, a.dx, a.dw, a.dbias, s->N, s->E, s->K,
-                               s->d, (s->flags & MOE_FLAG_OUT_BF16) ? 1 : 0};
-        const int blocks = (s->d + rb::kSmallCols - 1) / rb::kSmallCols;
+    if (rb::block_path(s->N, s->E, s->d)) {
+        const RouteBackLayout L = route_back_layout(s);
+        const int cols = (s->d + 63) / 64, tiles = (s->N + 63) / 64, parts = block_parts(s);
+        float *part = parts > 1 ? reinterpret_cast<float *>(ws + L.part) : a.dw;
+        float *bias = parts > 1 ? reinterpret_cast<float *>(ws + L.bias) : a.dbias;
+        const rb::BlockArgs b{in, a.x, a.w_router, a.dx_add, a.dx, a.dw ? part : nullptr,
+                              a.dbias ? bias : nullptr, s->N, s->E, s->K, s->d,
+                              (s->flags & MOE_FLAG_OUT_BF16) ? 1 : 0, cols, tiles, parts};
         moe_status_t rc = MOE_OK;
         row_lanes(s->E, [&](auto lpr) {
-            auto kern = rb::router_small_grad_kernel<decltype(lpr)::value>;
-            if (smem_attr_once(kern, rb::kSmallSmem) != cudaSuccess)
+            auto kern = rb::router_block_grad_kernel<decltype(lpr)::value>;
+            if (smem_attr_once(kern, rb::block_smem(kMaxE)) != cudaSuccess)
                 rc = MOE_ERR_CUDA;
             else
-                kern<<<blocks, 256, rb::small_smem(s->N, s->E), st>>>(sm);
+                kern<<<cols * parts, 256, rb::block_smem(s->E), st>>>(b);
         });
-        return rc != MOE_OK ? rc : launch_status();
+        if (rc != MOE_OK || parts == 1 || (!a.dw && !a.dbias))
+            return rc != MOE_OK ? rc : launch_status();
+        rb::SumArgs sum = {};
+        sum.d = s->d;
+        sum.E = s->E;
+        sum.parts = parts;
+        sum.part = part;
+        sum.dw = a.dw;
+        sum.bias_part = bias;
+        sum.bias_parts = parts;
+        sum.dbias = a.dbias;
+        return launch_router_sum(sum, st);
     }
     const RouteBackLayout L = route_back_layout(s);
     const DwGeometry g = dw_geometry(s);
@@ -1519,18 +1565,14 @@ moe_status_t route_backward_impl(const moe_shape_t *s, const RouteBackward &a, c
     sum.d = s->d;
     sum.E = s->E;
     sum.groups = g.groups;
-    sum.fold = s->E <= 64;
     sum.parts = g.parts;
+    sum.fold = s->E <= 64;
     sum.part = part;
     sum.dw = a.dw;
-    sum.dw_blocks = a.dw ? (int)(((int64_t)s->E * s->d / 4 + 255) / 256) : 0;
     sum.bias_part = bias;
     sum.bias_parts = sa.token_blocks;
     sum.dbias = a.dbias;
-    // not chained: its blocks, scheduled early beside dWr's, cost more than the launch they hide
-    // (128 experts, 8192 x 2048: 52 against 48 us in all)
-    rb::router_sum_kernel<<<sum.dw_blocks + (a.dbias ? (s->E + 7) / 8 : 0), 256, 0, st>>>(sum);
-    return launch_status();
+    return launch_router_sum(sum, st);
 }
 
 moe_status_t swiglu_backward_impl(const Geometry &g, int f, const uint8_t *ckpt,
@@ -1542,7 +1584,11 @@ moe_status_t swiglu_backward_impl(const Geometry &g, int f, const uint8_t *ckpt,
         ++tx;
     const int64_t ty = 256 >> tx, want = (g.rows_alloc + ty - 1) / ty;
     const int64_t most = 8 * (int64_t)num_sms();
-    swiglu_backward_kernel<<<(int)(want < most ? want : most), 256, 0, st>>>(
+    const unsigned rows = (unsigned)(want < most ? want : most);
+    // fewer blocks than four to an SM: a row's columns over several (200 rows of 11520: 27 -> 13 us)
+    const int64_t share = (4 * (int64_t)num_sms() + rows - 1) / rows, groups = (f / 8) >> tx;
+    const dim3 grid(rows, (unsigned)(share < groups ? share : groups));
+    swiglu_backward_kernel<<<grid, 256, 0, st>>>(
         ckpt, rows_dev, (int)g.rows_alloc, f, tx, dh, dgate, dup, h);
     return launch_status();
 }

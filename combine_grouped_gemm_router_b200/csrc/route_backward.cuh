@@ -14,7 +14,7 @@
 //   dx, fp32: hi hi + hi mid + mid hi + mid mid + hi lo + lo hi (what is left out is below
 //       2^-23 of the product); bf16: hi hi + hi mid + mid hi (below 2^-14, against the output's
 //       own rounding of 2^-8).
-// Four launches (one for a few tokens, router_small_grad_kernel): the split (router_split_grad_kernel), dx, dWr, and the sum of dWr's and dbias's
+// Four launches (one or two for little work, router_block_grad_kernel): the split (router_split_grad_kernel), dx, dWr, and the sum of dWr's and dbias's
 // partial results in a fixed order; the middle two are scheduled while the one before them drains
 // (grid_wait).
 // No atomics: the same bits every run.
@@ -633,8 +633,9 @@ __global__ void __launch_bounds__(kDwThreads, 1)
 
 struct SumArgs {
     int d, E;
-    int groups, parts;  // dWr's partial results [column tiles][groups][parts][32][128][8]
-    int fold;           // rows e and e + 64 of a partial result are both expert e's
+    // dWr's partial results: [column tiles][groups][parts][32][128][8] (router_dw_kernel; with fold,
+    // rows e and e + 64 of each are both expert e's), or, with groups = 0, [parts][E][d]
+    int groups, parts, fold;
     const float *part;
     float *dw;
     int dw_blocks;
@@ -643,31 +644,57 @@ struct SumArgs {
     float *dbias;
 };
 
-// dWr and dbias from their partial results, each element in the order of the tokens. A thread takes
-// 4 columns of an expert; neighbouring threads: the other 4 of a group of 8, then the next expert
-// (as the results lie).
+// dWr and dbias from their partial results, each element in a fixed order. SL threads share an
+// element group (4 neighbouring columns, as the results lie), every SL-th result each: 8 where
+// there are few groups (24634 x 152 x 9: 296 results of 342 groups), 1 where there are many.
+template <int SL>
 __global__ void __launch_bounds__(256) router_sum_kernel(const SumArgs a)
 {
     if ((int)blockIdx.x < a.dw_blocks) {
-        const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-        const int c8 = (int)(i / (2 * a.E)), r = (int)(i - (int64_t)c8 * (2 * a.E)), e = r >> 1;
-        if (c8 >= a.d / 8)
-            return;
-        const int tile = c8 / 32, group = e / 128;
-        const float *p = a.part + (size_t)(tile * a.groups + group) * a.parts * 32768 +
-                         (size_t)(c8 - tile * 32) * 1024 + (e - group * 128) * 8 + (r & 1) * 4;
-        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        constexpr int GROUPS = 256 / SL;
+        __shared__ float4 s_sum[SL][GROUPS];
+        const int slot = threadIdx.x % GROUPS, share = threadIdx.x / GROUPS;
         const int n = a.fold ? 2 * a.parts : a.parts;
-#pragma unroll 8
-        for (int k = 0; k < n; ++k) {
-            const float4 q = *reinterpret_cast<const float4 *>(
-                p + (a.fold ? (size_t)(k >> 1) * 32768 + (k & 1) * 512 : (size_t)k * 32768));
-            s.x += q.x;
-            s.y += q.y;
-            s.z += q.z;
-            s.w += q.w;
+        const int64_t i = (int64_t)blockIdx.x * GROUPS + slot;
+        const bool inside = i < (int64_t)a.E * a.d / 4;
+        size_t at = 4 * (size_t)i, to = at;  // of the result's first part; of dw
+        if (a.groups && inside) {
+            // 8 columns of an expert, half by half, then the next expert
+            const int c8 = (int)(i / (2 * a.E)), r = (int)(i - (int64_t)c8 * (2 * a.E)), e = r >> 1;
+            const int tile = c8 / 32, group = e / 128;
+            at = (size_t)(tile * a.groups + group) * a.parts * 32768 +
+                 (size_t)(c8 - tile * 32) * 1024 + (e - group * 128) * 8 + (r & 1) * 4;
+            to = (size_t)e * a.d + 8 * c8 + (r & 1) * 4;
         }
-        *reinterpret_cast<float4 *>(a.dw + (size_t)e * a.d + 8 * c8 + (r & 1) * 4) = s;
+        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (inside) {
+            const size_t step = a.groups ? 32768 : (size_t)a.E * a.d;
+#pragma unroll 8
+            for (int k = share; k < n; k += SL) {
+                const size_t off = a.fold ? (size_t)(k >> 1) * 32768 + (k & 1) * 512 : k * step;
+                const float4 q = *reinterpret_cast<const float4 *>(a.part + at + off);
+                s.x += q.x;
+                s.y += q.y;
+                s.z += q.z;
+                s.w += q.w;
+            }
+        }
+        if constexpr (SL > 1) {
+            s_sum[share][slot] = s;
+            __syncthreads();
+            if (share == 0) {
+#pragma unroll
+                for (int w = 1; w < SL; ++w) {
+                    const float4 q = s_sum[w][slot];
+                    s.x += q.x;
+                    s.y += q.y;
+                    s.z += q.z;
+                    s.w += q.w;
+                }
+            }
+        }
+        if (share == 0 && inside)
+            *reinterpret_cast<float4 *>(a.dw + to) = s;
         return;
     }
     // dbias: a warp per expert
@@ -1290,91 +1317,156 @@ __global__ void __launch_bounds__((DxTile<BF16, true, ADD>::THREADS), 1)
                      : "memory");
 }
 
-// ---------------------------------------------------------------- few tokens
+// ---------------------------------------------------------------- little work
 
-// A call of at most kSmallTokens tokens and kSmallLogits logits, whole, in one launch: launches
-// are what such a call costs. A block takes 32 columns of x; every block makes dl (in shared
-// memory) for itself, then its columns of dx and dWr in fp32; block 0 also sums dbias.
-constexpr int kSmallTokens = 256;
-constexpr int kSmallLogits = 8192;
-constexpr int kSmallCols = 32;
+// A call of little work (N E d <= kBlockWork) is bound by its launches and the latency of each: one
+// kernel makes dl, dx and dWr of 64 columns in fp32 on the FMA pipes, without planes and tensor
+// maps, and a second one adds the blocks' shares of dWr and dbias where there is more than one.
+// A block holds its 64 columns of the router weights and of 64 tokens at a time, makes dl of
+// those tokens for itself, and keeps its sums of dWr in registers over all its tokens (64
+// tokens in one run of additions, then those sums). Measured against the tensor-core path:
+// 64 x 128 x 8 13 against 26 us, 2575 x 136 x 11 15 against 19, 1000 x 1000 x 32
+// 18.5 against 20.5, 1024 x 2048 x 32 29 against 21.
+constexpr int64_t kBlockWork = (int64_t)1 << 25;
 
-struct SmallArgs {
+__host__ __device__ inline bool block_path(int N, int E, int d)
+{
+    return (int64_t)N * E * d <= kBlockWork;
+}
+
+struct BlockArgs {
     GradIn in;
     const uint16_t *x;
     const float *wr;
     const uint16_t *add;
     void *dx;
-    float *dw, *dbias;
+    float *dw;    // [parts][E][d]
+    float *bias;  // [E][parts]
     int N, E, K, d, bf16;
+    int cols, tiles, parts;  // tiles of 64 columns, of 64 tokens; shares of the latter
 };
 
-constexpr int small_smem(int N, int E) { return 4 * (N * E + kSmallCols * (N + E)); }
-// The most a call takes: N + E is largest where one of them is (256 tokens, or 256 experts).
-constexpr int kSmallSmem = small_smem(kSmallTokens, kSmallLogits / kSmallTokens);
-static_assert(kSmallSmem == small_smem(kSmallLogits / 256, 256), "E <= 256");
+// dl [64][E + 1] (a row's neighbours in other banks), x [64][64], Wr [E][64].
+constexpr int block_smem(int E) { return 4 * (64 * (E + 1) + 64 * 64 + 64 * E); }
 
 template <int LPR>
-__global__ void __launch_bounds__(256) router_small_grad_kernel(const SmallArgs a)
+__global__ void __launch_bounds__(256) router_block_grad_kernel(const BlockArgs a)
 {
-    extern __shared__ float small_smem_f[];
+    constexpr int GW = 32 / LPR, NI = LPR < 2 ? 1 : LPR / 2;  // experts of a thread: 16 apart
+    extern __shared__ __align__(16) float block_mem[];
     __shared__ __align__(16) float s_row[8 * 256];
-    constexpr int GW = 32 / LPR;
     const int N = a.N, E = a.E, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    float *dl = small_smem_f, *xs = dl + N * E, *ws = xs + N * kSmallCols;  // [N][E] [N][32] [E][32]
-    const int col = blockIdx.x * kSmallCols + lane;
-    for (int t0 = warp * GW; t0 < N; t0 += 8 * GW) {
-        const int l = lane % LPR, t = t0 + lane / LPR;
-        float v[8];
-        token_dlogits<LPR>(a.in, N, E, a.K, t, l, s_row + warp * 256 + (lane / LPR) * (8 * LPR), v);
-        if (t < N) {
+    float *xs = block_mem, *ws = xs + 64 * 64, *dl = ws + 64 * E;
+    const int tx = tid & 15, ty = tid >> 4, pitch = E + 1;
+    const int tile_c = blockIdx.x % a.cols, part = blockIdx.x / a.cols;
+    const int c0 = tile_c * 64, col = c0 + 4 * tx;  // this thread's 4 columns
+    const int t_first = (int)((int64_t)a.tiles * part / a.parts);
+    const int t_last = (int)((int64_t)a.tiles * (part + 1) / a.parts);
+    if (a.dx)
+        for (int i = tid; i < E * 16; i += 256) {
+            const int e = i >> 4, c = c0 + 4 * (i & 15);
+            *reinterpret_cast<float4 *>(ws + e * 64 + 4 * (i & 15)) =
+                c < a.d ? *reinterpret_cast<const float4 *>(a.wr + (size_t)e * a.d + c)
+                        : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+    float sum[NI][4] = {}, bias = 0.0f;
+    for (int tile = t_first; tile < t_last; ++tile) {
+        const int t0 = tile * 64;
+        __syncthreads();  // the tile before is done with
+        for (int r = warp * GW; r < 64; r += 8 * GW) {
+            const int l = lane % LPR, t = r + lane / LPR;
+            float v[8];
+            token_dlogits<LPR>(a.in, N, E, a.K, t0 + t, l, s_row + warp * 256 + (lane / LPR) * (8 * LPR),
+                               v);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 if (8 * l + j < E)
-                    dl[t * E + 8 * l + j] = v[j];
+                    dl[t * pitch + 8 * l + j] = v[j];
         }
-    }
-    if (a.dw)
-        for (int t = warp; t < N; t += 8)
-            xs[t * kSmallCols + lane] =
-                col < a.d && (!a.in.mask || a.in.mask[t])
-                    ? __uint_as_float((uint32_t)a.x[(size_t)t * a.d + col] << 16)
-                    : 0.0f;
-    if (a.dx)
-        for (int e = warp; e < E; e += 8)
-            ws[e * kSmallCols + lane] = col < a.d ? a.wr[(size_t)e * a.d + col] : 0.0f;
-    __syncthreads();
-    if (a.dx && col < a.d) {
-        for (int t = warp; t < N; t += 8) {
-            float s = 0.0f;
+        if (a.dw)
+            for (int i = tid; i < 64 * 8; i += 256) {  // 8 columns of a token
+                const int t = t0 + (i >> 3), c = c0 + 8 * (i & 7);
+                uint4 q = make_uint4(0, 0, 0, 0);
+                if (t < N && c < a.d && (!a.in.mask || a.in.mask[t]))
+                    q = *reinterpret_cast<const uint4 *>(a.x + (size_t)t * a.d + c);
+                float4 *o = reinterpret_cast<float4 *>(xs + (i >> 3) * 64 + 8 * (i & 7));
+                o[0] = make_float4(bf16_lo(q.x), bf16_hi(q.x), bf16_lo(q.y), bf16_hi(q.y));
+                o[1] = make_float4(bf16_lo(q.z), bf16_hi(q.z), bf16_lo(q.w), bf16_hi(q.w));
+            }
+        __syncthreads();
+        if (a.dx) {
+            float acc[4][4] = {};  // tokens ty + 16 i
+#pragma unroll 4
+            for (int e = 0; e < E; ++e) {
+                const float4 w = *reinterpret_cast<const float4 *>(ws + e * 64 + 4 * tx);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float g = dl[(ty + 16 * i) * pitch + e];
+                    acc[i][0] = fmaf(g, w.x, acc[i][0]);
+                    acc[i][1] = fmaf(g, w.y, acc[i][1]);
+                    acc[i][2] = fmaf(g, w.z, acc[i][2]);
+                    acc[i][3] = fmaf(g, w.w, acc[i][3]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = t0 + ty + 16 * i;
+                if (t >= N || col >= a.d)
+                    continue;
+                const size_t at = (size_t)t * a.d + col;
+                if (a.add) {
+                    const uint2 q = *reinterpret_cast<const uint2 *>(a.add + at);
+                    acc[i][0] += bf16_lo(q.x);
+                    acc[i][1] += bf16_hi(q.x);
+                    acc[i][2] += bf16_lo(q.y);
+                    acc[i][3] += bf16_hi(q.y);
+                }
+                if (a.bf16)
+                    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.dx) + at) = make_uint2(
+                        pack_bf16x2(acc[i][0], acc[i][1]), pack_bf16x2(acc[i][2], acc[i][3]));
+                else
+                    *reinterpret_cast<float4 *>(static_cast<float *>(a.dx) + at) =
+                        make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+            }
+        }
+        if (a.dw) {
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int e = min(ty + 16 * i, E - 1);
+                float acc[4] = {};
 #pragma unroll 8
-            for (int e = 0; e < E; ++e)
-                s = fmaf(dl[t * E + e], ws[e * kSmallCols + lane], s);
-            const size_t at = (size_t)t * a.d + col;
-            if (a.add)
-                s += __uint_as_float((uint32_t)a.add[at] << 16);
-            if (a.bf16)
-                static_cast<uint16_t *>(a.dx)[at] = (uint16_t)pack_bf16x2(s, 0.0f);
-            else
-                static_cast<float *>(a.dx)[at] = s;
+                for (int t = 0; t < 64; ++t) {
+                    const float g = dl[t * pitch + e];
+                    const float4 q = *reinterpret_cast<const float4 *>(xs + t * 64 + 4 * tx);
+                    acc[0] = fmaf(g, q.x, acc[0]);
+                    acc[1] = fmaf(g, q.y, acc[1]);
+                    acc[2] = fmaf(g, q.z, acc[2]);
+                    acc[3] = fmaf(g, q.w, acc[3]);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    sum[i][j] += acc[j];
+            }
+        }
+        if (a.bias && tile_c == 0 && tid < E) {
+            float acc = 0.0f;
+#pragma unroll 8
+            for (int t = 0; t < 64; ++t)
+                acc += dl[t * pitch + tid];
+            bias += acc;
         }
     }
     if (a.dw && col < a.d) {
-        for (int e = warp; e < E; e += 8) {
-            float s = 0.0f;
-#pragma unroll 8
-            for (int t = 0; t < N; ++t)
-                s = fmaf(dl[t * E + e], xs[t * kSmallCols + lane], s);
-            a.dw[(size_t)e * a.d + col] = s;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int e = ty + 16 * i;
+            if (e < E)
+                *reinterpret_cast<float4 *>(a.dw + ((size_t)part * E + e) * a.d + col) =
+                    make_float4(sum[i][0], sum[i][1], sum[i][2], sum[i][3]);
         }
     }
-    if (a.dbias && blockIdx.x == 0 && tid < E) {
-        float s = 0.0f;
-#pragma unroll 8
-        for (int t = 0; t < N; ++t)
-            s += dl[t * E + tid];
-        a.dbias[tid] = s;
-    }
+    if (a.bias && tile_c == 0 && tid < E)
+        a.bias[(size_t)tid * a.parts + part] = bias;
 }
 
 }  // namespace rb

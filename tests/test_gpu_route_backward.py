@@ -94,7 +94,10 @@ SHAPES = [(1, 8, 1, 1), (1, 128, 256, 8), (2, 24, 3, 2), (63, 136, 8, 2), (64, 1
           (700, 2048, 256, 8), (4097, 128, 40, 2),
           # the tensor-core path on narrow and ragged x, on E just past 64 and 128
           (260, 8, 3, 2), (1000, 24, 100, 4), (258, 40, 65, 1), (385, 200, 129, 3),
-          (2000, 328, 64, 1), (515, 1032, 33, 32)]
+          (2000, 328, 64, 1), (515, 1032, 33, 32),
+          # beyond the little-work path: E to 64, 128, 256, ragged in every direction
+          (9001, 152, 50, 3), (5003, 264, 64, 6), (4099, 1000, 20, 2), (3001, 328, 100, 4),
+          (2100, 392, 129, 5), (1500, 776, 65, 8), (1100, 1064, 193, 8), (1300, 512, 256, 4)]
 
 
 @pytest.mark.parametrize("bf16", [False, True])
