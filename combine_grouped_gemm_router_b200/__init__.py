@@ -519,9 +519,9 @@ def moe_route_backward(shape, x, w_router, dx, dw_router, dbias=None, topk_idx=N
     dbias."""
     N, E, NK = shape.N, shape.E, shape.N * shape.K
     Nd, Ed = N * shape.d, E * shape.d
-    p = _args("moe_route_backward", stream, ("x", x, _T.bf16, Nd), ("w_router", w_router, _T.f32, Ed),
-              ("topk_idx", topk_idx, _T.i32, NK), ("topk_w", topk_w, _T.f32, NK),
-              ("dtopk_w", dtopk_w, _T.f32, NK), ("dlogits", dlogits, _T.f32, N * E),
+    p = _args("moe_route_backward", stream, ("x", x, _T.bf16, Nd),
+              ("w_router", w_router, _T.f32, Ed), ("topk_idx", topk_idx, _T.i32, NK),
+              ("topk_w", topk_w, _T.f32, NK), ("dtopk_w", dtopk_w, _T.f32, NK), ("dlogits", dlogits, _T.f32, N * E),
               ("token_mask", token_mask, _T.mask, N), ("dx_add", dx_add, _T.bf16, Nd),
               ("dx", dx, _T.bf16 if shape.flags & MOE_FLAG_OUT_BF16 else _T.f32, Nd),
               ("dw_router", dw_router, _T.f32, Ed), ("dbias", dbias, _T.f32, E),

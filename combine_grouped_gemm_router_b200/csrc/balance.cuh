@@ -320,7 +320,9 @@ __global__ void __cluster_dims__(kFinishBlocks, 1, 1) __launch_bounds__(1024, 1)
         const double term = warp_sum((double)c / out.K * inv_m * mean);
         if (lane == 0) {  // to the first block
             uint32_t at;
-            asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(smem_u32(&s_term[blockIdx.x])));
+            asm volatile("mapa.shared::cluster.u32 %0, %1, 0;"
+                         : "=r"(at)
+                         : "r"(smem_u32(&s_term[blockIdx.x])));
             asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(at), "d"(term) : "memory");
         }
     }

@@ -14,10 +14,10 @@
 //   dx, fp32: hi hi + hi mid + mid hi + mid mid + hi lo + lo hi (what is left out is below
 //       2^-23 of the product); bf16: hi hi + hi mid + mid hi (below 2^-14, against the output's
 //       own rounding of 2^-8).
-// Four launches (one or two for little work, router_block_grad_kernel): the split (router_split_grad_kernel), dx, dWr, and the sum of dWr's and dbias's
-// partial results in a fixed order; the middle two are scheduled while the one before them drains
-// (grid_wait).
-// No atomics: the same bits every run.
+// Four launches (one or two for little work, router_block_grad_kernel): the split
+// (router_split_grad_kernel), dx, dWr, and the sum of dWr's and dbias's partial results in a
+// fixed order; the middle two are scheduled while the one before them drains (grid_wait). No
+// atomics: the same bits every run.
 #pragma once
 
 #include "balance.cuh"
@@ -158,8 +158,9 @@ __device__ __forceinline__ void token_dlogits(const GradIn &in, int N, int E, in
         }
         const float g = w * (dw - s);
         // an expert twice among these slots (no router's top-K, but allowed): one after another
-        const uint32_t same = __match_any_sync(0xffffffffu, idx < 0 ? -1 - (int)(threadIdx.x & 31)
-                                                                    : idx + (((threadIdx.x & 31) / LPR) << 16));
+        const int self = threadIdx.x & 31;
+        const int key = idx < 0 ? -1 - self : idx + ((self / LPR) << 16);
+        const uint32_t same = __match_any_sync(0xffffffffu, key);
         const bool lone = (same & (same - 1)) == 0;
         if (__all_sync(0xffffffffu, lone)) {
             if (idx >= 0)
@@ -326,9 +327,10 @@ __device__ __forceinline__ bool elect_one()
 // N is (measured: 70 at N = 64 and 128, 130 at 256: its A operand is read at 64 bytes a
 // cycle), so the wide side has to be N. Up to 64 experts (FOLD), the M tile holds two planes
 // (rows e: hi and lo, rows 64 + e: mid), which router_sum_kernel adds; the fourth quarter of A is a
-// box of zeros. More experts: a CTA takes 128 of them. A chunk's sum is read back and added to fp32 registers before it is longer than 128
-// tokens: the tensor core's accumulator truncates, and a truncation per step over tens of
-// thousands of tokens would cost the low bits that the split keeps.
+// box of zeros. More experts: a CTA takes 128 of them. A chunk's sum is read back and added to
+// fp32 registers before it is longer than 128 tokens: the tensor core's accumulator truncates,
+// and a truncation per step over tens of thousands of tokens would cost the low bits that the
+// split keeps. 32768 x 4096 x 64: 57 us, 4.7 TB/s of x, MMA 0.6 of the time.
 // The CTAs of one share of the tokens walk over them together, one column tile each, so that
 // rows of x are read whole within a short time.
 constexpr int kChunk = 128;  // tokens accumulated in TMEM
@@ -552,8 +554,9 @@ __global__ void __launch_bounds__(kDwThreads, 1)
                     break;
                 if (__any_sync(0xffffffffu, now)) {
 #pragma unroll
-                    for (int i = 0; i < TOK / 32; ++i)
-                        for (uint32_t m = __ballot_sync(0xffffffffu, now >> i & 1u); m; m &= m - 1) {
+                    for (int i = 0; i < TOK / 32; ++i) {
+                        uint32_t m = __ballot_sync(0xffffffffu, now >> i & 1u);
+                        for (; m; m &= m - 1) {
                             // a row of each of the XB boxes: 128 bytes, 8 lanes
                             const int row = 32 * i + __ffs(m) - 1;
                             if (lane < 8 * XB) {
@@ -564,6 +567,7 @@ __global__ void __launch_bounds__(kDwThreads, 1)
                                              : "memory");
                             }
                         }
+                    }
                     gg::fence_proxy_async_smem();
                     __syncwarp();
                 }
@@ -612,8 +616,8 @@ __global__ void __launch_bounds__(kDwThreads, 1)
         // writes 1 KB in one piece
         const int row = q * 32 + lane;
         if ((FOLD ? (row & 63) : group * 128 + row) < a.E) {
-            float *dst = a.part + ((size_t)(tile * a.groups + group) * a.parts + part) * (128 * 64 * XB) +
-                         (size_t)(half * 16) * 1024 + row * 8;
+            const size_t result = (size_t)(tile * a.groups + group) * a.parts + part;
+            float *dst = a.part + result * (128 * 64 * XB) + half * 16 * 1024 + row * 8;
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
                 float4 *o = reinterpret_cast<float4 *>(dst + j * 1024);
@@ -633,8 +637,8 @@ __global__ void __launch_bounds__(kDwThreads, 1)
 
 struct SumArgs {
     int d, E;
-    // dWr's partial results: [column tiles][groups][parts][32][128][8] (router_dw_kernel; with fold,
-    // rows e and e + 64 of each are both expert e's), or, with groups = 0, [parts][E][d]
+    // dWr's partial results: [column tiles][groups][parts][32][128][8] (router_dw_kernel; with
+    // fold, rows e and e + 64 of each are both expert e's), or, with groups = 0, [parts][E][d]
     int groups, parts, fold;
     const float *part;
     float *dw;
@@ -719,11 +723,12 @@ __global__ void __launch_bounds__(256) router_sum_kernel(const SumArgs a)
 // j <= PLANES - 1 - i of the weights; eight epilogue warps. The CTAs of a group hold the column
 // slices of x and walk over the tokens together, so rows of dx are written whole within a
 // short time (measured against CTAs that each walk a strip of their own: 90 -> 74 us at
-// 32768 x 4096).
+// 32768 x 4096 x 64; 52 us now, 86 with dx_add: 541 MB at 6.2 TB/s).
 // More experts (router_dx_pair_kernel): the weights' planes do not fit beside the rest, so both
 // operands stream, 32 experts a stage. A pair of CTAs computes 256 tokens x 256 columns
 // (cta_group::2): each loads its 128 tokens of dl and half of the columns of the weights, which
-// both read.
+// both read. Bound by those reads through L2 (about 40 bytes a cycle and SM): 64 us at
+// 16384 x 4096 x 128, 39 at 4001 x 7168 x 256 (fp32: 70).
 constexpr int kUnit = 16384;   // 128 tokens x 64 experts, bf16
 constexpr int kPiece = 4096;   // 32 tokens x 128 bytes of dx: what one warp stores at a time
 constexpr int kDxMaxUnits = 6;
@@ -746,7 +751,10 @@ struct DxTile {
     {
         return PAIR ? PLANES * (8192 + nb / 2 * 4096) : kUnit;
     }
-    __host__ __device__ static constexpr int weights(int nb) { return PAIR ? 0 : PLANES * nb * kBox; }
+    __host__ __device__ static constexpr int weights(int nb)  // bytes of the weights kept
+    {
+        return PAIR ? 0 : PLANES * nb * kBox;
+    }
 };
 
 struct DxArgs {
@@ -762,8 +770,9 @@ struct DxArgs {
 // quadrant take turns at the pieces of a tile. item(i, tile, slice): this CTA's i-th tile of
 // `mine`; release(acc): the accumulator has been read.
 template <typename T, bool ADD, typename Item, typename Release>
-__device__ __forceinline__ void dx_epilogue(const DxArgs &a, uint32_t tmem, uint32_t p_base, int mine,
-                                            const CUtensorMap &tm_dx, const CUtensorMap &tm_add,
+__device__ __forceinline__ void dx_epilogue(const DxArgs &a, uint32_t tmem, uint32_t p_base,
+                                            int mine, const CUtensorMap &tm_dx,
+                                            const CUtensorMap &tm_add,
                                             uint32_t tfull0, uint32_t addfull0,
                                             volatile int *abort_flag, const Item &item,
                                             const Release &release)
@@ -779,7 +788,7 @@ __device__ __forceinline__ void dx_epilogue(const DxArgs &a, uint32_t tmem, uint
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
     const uint32_t slots = p_base + w * SLOTS * kPiece;
     const uint32_t adds = BF16 ? slots : p_base + EW * SLOTS * kPiece + w * SLOTS * T::ADD_SLOT;
-    const int pieces = 64 * nb / CP;                             // of a tile
+    const int pieces = 64 * nb / CP;                      // of a tile
     const int own = (pieces - turn + TURNS - 1) / TURNS;  // of them, this warp's
     // a piece's column and first token (of the warp's 32); the pieces of a warp follow one
     // another over the tiles, and their slots and barrier phases with them
@@ -806,7 +815,8 @@ __device__ __forceinline__ void dx_epilogue(const DxArgs &a, uint32_t tmem, uint
     auto fetch = [&]() {
         const uint32_t bar = addfull(w, ahead.slot);
         mbar_arrive_expect_tx(bar, T::ADD_SLOT);
-        gg::tma_load_2d(adds + ahead.slot * T::ADD_SLOT, &tm_add, col_of(ahead), row_of(ahead), bar);
+        gg::tma_load_2d(adds + ahead.slot * T::ADD_SLOT, &tm_add, col_of(ahead), row_of(ahead),
+                        bar);
         next(ahead);
     };
     int fetched = 0, used = 0;
@@ -1376,8 +1386,8 @@ __global__ void __launch_bounds__(256) router_block_grad_kernel(const BlockArgs 
         for (int r = warp * GW; r < 64; r += 8 * GW) {
             const int l = lane % LPR, t = r + lane / LPR;
             float v[8];
-            token_dlogits<LPR>(a.in, N, E, a.K, t0 + t, l, s_row + warp * 256 + (lane / LPR) * (8 * LPR),
-                               v);
+            float *row = s_row + warp * 256 + (lane / LPR) * (8 * LPR);
+            token_dlogits<LPR>(a.in, N, E, a.K, t0 + t, l, row, v);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 if (8 * l + j < E)

@@ -190,7 +190,8 @@ def test_bad_values_are_flagged():
     twice = idx.copy()
     twice[:, 1] = twice[:, 0]
     call(m, shape, cuda(logits), cuda(twice), o)
-    np.testing.assert_array_equal(o["counts"].cpu().numpy(), np.bincount(twice.reshape(-1), minlength=E))
+    np.testing.assert_array_equal(o["counts"].cpu().numpy(),
+                                  np.bincount(twice.reshape(-1), minlength=E))
     assert m.moe_get_device_error(True) == 0
 
 

@@ -190,7 +190,7 @@ def test_gate_gradient_against_differences():
             assert abs((got * v).sum() - diff) <= 2e-5 * np.abs(got * v).sum() + 1e-9
 
 
-@pytest.mark.parametrize("E,bf16", [(64, True), (200, False)])
+@pytest.mark.parametrize("E,bf16", [(64, True), (200, False), (64, False), (200, True)])
 def test_repeats_streams_and_graphs(E, bf16):
     """The same bits on every run, on another stream, from a graph's replay over new inputs, and
     with a bf16 dx written over dx_add."""
