@@ -285,6 +285,8 @@ __global__ void __cluster_dims__(kFinishBlocks, 1, 1) __launch_bounds__(1024, 1)
     __shared__ double s_term[kFinishBlocks];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, E = out.E;
     const int e = blockIdx.x * 32 + lane;
+    // every block of the cluster has started before one writes to another's shared memory
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
     grid_wait();
     double p = 0.0, z = 0.0;
     int c = 0, m = 0;
