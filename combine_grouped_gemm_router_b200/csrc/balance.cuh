@@ -91,7 +91,9 @@ __device__ __forceinline__ float row_sum(float v)
 // Softmax of the row in v, in place: exponentials relative to the row's maximum, not yet divided
 // by their sum. Returns the sum; lse: the log-sum-exp. With L = log2(e), e^(v - m) is
 // 2^(v L - m L), one fused multiply-add: the rounding of m L is common to the row and cancels in
-// the probabilities. Results below fp32's normal range are 0.
+// the probabilities. That holds while it is small against 1: a row whose maximum is past 2^20
+// (m L off by up to 2^-4 there, by infinity at the type's lowest value) subtracts m first.
+// Results below fp32's normal range are 0.
 template <int LPR, int C>
 __device__ __forceinline__ float row_softmax(float (&v)[C], float &lse)
 {
@@ -101,7 +103,14 @@ __device__ __forceinline__ float row_softmax(float (&v)[C], float &lse)
     for (int j = 1; j < C; ++j)
         m = fmaxf(m, v[j]);
     m = row_max<LPR>(m);
-    const float c = -m * kL;
+    float c = -m * kL;
+    if (fabsf(m) > 1048576.0f) {
+#pragma unroll
+        for (int j = 0; j < C; ++j)
+            v[j] -= m;
+        c = 0.0f;
+    }
+    __syncwarp();
     float s = 0.0f;
 #pragma unroll
     for (int j = 0; j < C; ++j) {
@@ -154,7 +163,7 @@ __device__ __forceinline__ void balance_outputs(const BalanceOut &o, double prob
             bal += red[w];
         bal *= o.E;
         const double zz = z * inv_m;
-        o.loss[0] = (float)(o.cb * bal + o.cz * zz);
+        o.loss[0] = (float)(o.cb * bal + (o.cz != 0.0f ? o.cz * zz : 0.0));  // zz may be inf
         o.loss[1] = (float)bal;
         o.loss[2] = (float)zz;
         o.tokens[0] = tokens;
@@ -335,7 +344,7 @@ __global__ void __cluster_dims__(kFinishBlocks, 1, 1) __launch_bounds__(1024, 1)
             bal += s_term[r];
         const double inv_m = m > 0 ? 1.0 / m : 0.0, zz = z * inv_m;
         bal *= E;
-        out.loss[0] = (float)(out.cb * bal + out.cz * zz);
+        out.loss[0] = (float)(out.cb * bal + (out.cz != 0.0f ? out.cz * zz : 0.0));
         out.loss[1] = (float)bal;
         out.loss[2] = (float)zz;
         out.tokens[0] = m;

@@ -538,7 +538,9 @@ size_t moe_balance_workspace_size(const moe_shape_t *shape);
  * logits [N][E] fp32 and topk_idx [N][K] as moe_route wrote them. Outputs (DEVICE): loss [3]
  * fp32, counts [E] int32, prob_mean [E] fp32, tokens [1] int32 = M; all 0 when M = 0.
  * fp32 softmax, fp32 sums within a thread, fp64 across blocks; the same bits every run.
- * A logit of -inf has probability 0. A counted token with a NaN or +inf logit (or only -inf)
+ * A logit of -inf, or of the type's lowest value beside larger ones, has probability 0. lse_t^2
+ * may pass fp32 (|lse_t| > 2^63): loss[2] is then inf, and loss[0] too unless z_coef = 0.
+ * A counted token with a NaN or +inf logit (or only -inf)
  * makes the loss NaN or infinite and sets MOE_ERR_NONFINITE; an entry of topk_idx outside
  * [0, E) is not counted and sets MOE_ERR_DEVICE_BOUNDS. The coefficients must be finite.
  * ws: moe_balance_workspace_size bytes, 16-byte aligned, contents irrelevant before and after;

@@ -145,6 +145,59 @@ def test_minus_infinity_is_probability_zero():
     assert m.moe_get_device_error(True) == 0
 
 
+@pytest.mark.parametrize("N,E,K,cz", [(42, 8, 2, 0.0), (42, 8, 2, 1e-3), (300, 13, 3, 0.0),
+                                      (700, 160, 6, 1e-3), (20011, 64, 6, 0.0),
+                                      (9001, 255, 8, 1e-3)])
+def test_large_finite_logits(N, E, K, cz):
+    """Experts switched off by the type's lowest value (a whole row of it included) and rows far
+    from 0. Every difference to a row's maximum is exact in fp32 or so large that its probability
+    is 0, so a probability is within PREL of X <= 88, or 2^-126 where it underflows. lse^2 passes
+    fp32 in the rows that z_coef = 0 brings: loss[2] is inf there and loss[0] does not see it."""
+    m = lib()
+    rng, logits, _, _ = inputs(N, E, K, 31)
+    logits = np.round(logits * 4) / 4
+    kind = np.arange(N) % 7
+    lowest, highest = np.finfo(np.float32).min, np.finfo(np.float32).max
+    half = rng.random((N, E)) < 0.5
+    half[:, 0] = False
+    logits[kind == 0] -= 2.0 ** 21
+    logits[kind == 1] = np.where(half, 3e9, 3e9 + 512)[kind == 1]
+    logits[kind == 2] = np.where(half, lowest, logits)[kind == 2]
+    logits[kind == 3] += 3.0 * 2.0 ** 20
+    if cz == 0.0:
+        logits[kind == 4] = lowest
+        logits[kind == 5] = np.where(half, lowest, highest)[kind == 5]
+        logits[kind == 6] = np.where(half, -1e30, 1e30)[kind == 6]
+    logits = logits.astype(np.float32)
+    idx, _ = topk_of(logits, K)
+    shape = m.make_shape(N, 128, 128, E, K, 1)
+    o = outputs(E, N)
+    call(m, shape, cuda(logits), cuda(idx), o, cb=1e-2, cz=cz)
+    m.moe_balance_loss_backward(shape, cuda(logits), o["counts"], o["tokens"], o["dlogits"],
+                                balance_coef=1e-2, z_coef=cz)
+    assert m.moe_get_device_error(True) == 0
+    ref = balance(logits, idx, None, 1e-2, cz)
+    prel = 2.0 ** -19 + 88 * 2.0 ** -23
+    rel = prel + (N + 64) * 2.0 ** -24          # as in check_loss
+    mean, loss = f64(o["mean"]), f64(o["loss"])
+    assert np.all(np.abs(mean - ref["prob_mean"]) <= rel * ref["prob_mean"] + 2.0 ** -126)
+    # lse: 2^-24 of itself from the addition and less than 2^-20 from the logarithm; squared
+    want = ref["loss"].copy()
+    if cz == 0.0:
+        assert loss[2] == np.inf
+    else:
+        assert abs(loss[2] - want[2]) <= (2.0 ** -18 + rel) * want[2]
+    for i in (0, 1):
+        assert abs(loss[i] - want[i]) <= (2.0 ** -18 + rel) * abs(want[i])
+    a, b = 1e-2 * E / N, cz * 2.0 / N
+    inner = (ref["p"] @ ref["share"])[:, None]
+    lse = ref["lse"][:, None]
+    exact = ref["p"] * (a * (ref["share"] - inner) + b * lse)
+    size = ref["p"] * (a * (ref["share"] + inner) + b * np.abs(lse))
+    assert np.all(np.abs(f64(o["dlogits"]) - exact) <= size * (3 * prel + 2.0 ** -20)
+                  + (a + b * np.abs(lse)) * 2.0 ** -125)
+
+
 @pytest.mark.parametrize("N", [40, 5000])
 def test_nothing_counted(N):
     """Every token masked, or none at all: zeros, and a zero gradient."""
