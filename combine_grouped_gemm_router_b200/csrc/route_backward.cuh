@@ -528,8 +528,10 @@ __global__ void __launch_bounds__(kDwThreads, 1)
         }
     } else if (warp < 4) {
         if (a.mask) {
-            // two warps, every other stage each; the mask bytes of a warp's next stage are loaded
-            // while this one is awaited
+            // Two warps, every other stage of the ring each, and a stage the same warp's at every
+            // use: loads land in any order, and a wait by parity tells a phase from its
+            // neighbours only, so whoever waits for a stage must have seen its use before.
+            // The mask bytes of a warp's next stage are loaded while this one is awaited.
             const int64_t t_end = min((int64_t)c1 * kChunk, (int64_t)a.N);
             auto masked = [&](int64_t t0) {  // bit i: token t0 + 32 i + lane
                 uint32_t m = 0;
@@ -540,15 +542,17 @@ __global__ void __launch_bounds__(kDwThreads, 1)
                 return m;
             };
             int ok = 1;
-            int64_t t0 = (int64_t)c0 * kChunk + (warp - 2) * TOK;
+            int stage = warp - 2;
+            uint32_t phase = 0;
+            int64_t t0 = (int64_t)c0 * kChunk + stage * TOK;
             uint32_t next = masked(t0);
-            for (int n = warp - 2; t0 < t_end; n += 2, t0 += 2 * TOK) {
-                const int stage = n % S;
+            while (t0 < t_end) {
+                const bool wraps = stage + 2 >= S;
+                const int64_t t1 = t0 + (wraps ? S - stage + warp - 2 : 2) * TOK;
                 const uint32_t now = next;
-                next = masked(t0 + 2 * TOK);
+                next = masked(t1);
                 if (lane == 0)
-                    ok = gg::mbar_wait(full(stage), (uint32_t)(n / S) & 1u, abort_flag,
-                                       a.timeout_ns) ? 1 : 0;
+                    ok = gg::mbar_wait(full(stage), phase, abort_flag, a.timeout_ns) ? 1 : 0;
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok)
                     break;
@@ -573,6 +577,9 @@ __global__ void __launch_bounds__(kDwThreads, 1)
                 }
                 if (lane == 0)
                     mbar_arrive(clean(stage));
+                t0 = t1;
+                stage = wraps ? warp - 2 : stage + 2;
+                phase ^= (uint32_t)wraps;
             }
         }
     } else if (warp >= 4) {
