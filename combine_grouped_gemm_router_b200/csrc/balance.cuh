@@ -10,15 +10,22 @@
 //
 // Both passes read the [N][E] logits once. A row is held by LPR lanes, up to 16 columns each, so
 // the softmax's maximum and sum are log2(LPR) shuffles and a lane owns the same columns in every
-// row it sees: the sums over tokens stay in its registers until the end of the block. Issue
-// slots bound the passes: with 8 columns a lane the shuffles were a third of the instructions.
+// row it sees: the sums over tokens stay in its registers until the end of the block. With 8
+// columns a lane the shuffles were a third of the instructions. The sums (131072 x 256 with a
+// mask: 33 us, of which 4 in balance_finish_kernel) read the next row's logits while a row is
+// worked on; their loop streams at about 6 TB/s, the rest is the start and the end of the two
+// kernels. The gradient (30011 x 160: 11 us) is bound by issue slots: what can be done to two
+// columns by one instruction is (12 us one by one).
 #pragma once
 
 #include "common.cuh"
 
 namespace moe {
 
-constexpr int kBalThreads = 1024;
+// Registers for two rows a lane; 131072 x 256: 33.0 us, 33.7 with 768, 36.6 with 1024 (64
+// registers a thread are too few), 36.8 with 640. A ring of rows in shared memory instead of
+// the registers: 35.4.
+constexpr int kBalThreads = 896;
 
 // Lane l of the LPR lanes of a row holds C = 4 NC columns col(j): NC 16-byte chunks (VEC,
 // E % 4 == 0) or C columns LPR apart. A column at or past E reads as -inf (probability 0).
@@ -71,6 +78,34 @@ struct RowSlice {
     }
 };
 
+// Two fp32 values in a register pair: one instruction for both.
+struct Pair {
+    unsigned long long r;
+    __device__ __forceinline__ Pair(float lo, float hi)
+    {
+        asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    }
+    __device__ __forceinline__ void get(float &lo, float &hi) const
+    {
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(r));
+    }
+};
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c)  // a b + c
+{
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c.r) : "l"(a.r), "l"(b.r));
+    return c;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b)
+{
+    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a.r) : "l"(b.r));
+    return a;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b)
+{
+    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(a.r) : "l"(b.r));
+    return a;
+}
+
 template <int LPR>
 __device__ __forceinline__ float row_max(float v)
 {
@@ -111,13 +146,18 @@ __device__ __forceinline__ float row_softmax(float (&v)[C], float &lse)
         c = 0.0f;
     }
     __syncwarp();
-    float s = 0.0f;
+    Pair sum(0.0f, 0.0f);
 #pragma unroll
-    for (int j = 0; j < C; ++j) {
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(v[j]) : "f"(fmaf(v[j], kL, c)));
-        s += v[j];
+    for (int j = 0; j < C; j += 2) {
+        float a, b;
+        fma2(Pair(v[j], v[j + 1]), Pair(kL, kL), Pair(c, c)).get(a, b);
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(v[j]) : "f"(a));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(v[j + 1]) : "f"(b));
+        sum = add2(sum, Pair(v[j], v[j + 1]));
     }
-    s = row_sum<LPR>(s);
+    float s, s1;
+    sum.get(s, s1);
+    s = row_sum<LPR>(s + s1);
     float l2;
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(l2) : "f"(s));
     lse = fmaf(l2, kLn2, m);
@@ -199,30 +239,52 @@ __global__ void __launch_bounds__(kBalThreads, 1)
     int m_tok = 0;
     bool bad_index = false, bad_logit = false;
     const int64_t stride = (int64_t)gridDim.x * WARPS * GW;
-    for (int64_t base = ((int64_t)blockIdx.x * WARPS + warp) * GW; base < N; base += stride) {
-        const int64_t t = base + grp;
-        const bool inside = t < N, live = inside && (!mask || mask[t]);
+    // a row is loaded while the one before it is worked on
+    struct {
         float v[C];
-        Slice::load(logits + (inside ? t : 0) * E, inside ? E : 0, l, v);
+        int e;  // this lane's first slot
+        bool inside, live;
+    } next;
+    auto fetch = [&](int64_t base) {
+        const int64_t t = base + grp;
+        next.inside = t < N;
+        next.live = next.inside && (!mask || mask[t]);
+        Slice::load(logits + (next.inside ? t : 0) * E, next.inside ? E : 0, l, next.v);
+        next.e = next.inside && l < K ? topk_idx[t * K + l] : 0;
+    };
+    int64_t base = ((int64_t)blockIdx.x * WARPS + warp) * GW;
+    if (base < N)
+        fetch(base);
+    for (; base < N; base += stride) {
+        const int64_t t = base + grp;
+        const bool inside = next.inside, live = next.live;
+        const int first = next.e;
+        float v[C];
+#pragma unroll
+        for (int j = 0; j < C; ++j)
+            v[j] = next.v[j];
+        if (base + stride < N)
+            fetch(base + stride);
         // counts: lane l takes the slots l, l + LPR, ... of its token
         for (int k = l; k < K; k += LPR) {
-            const int e = inside ? topk_idx[t * K + k] : 0;
+            const int e = k == l ? first : inside ? topk_idx[t * K + k] : 0;
             const bool ok = (unsigned)e < (unsigned)E;
             if (live && ok)
                 atomicAdd(&s_count[e], 1);
             bad_index |= live && !ok;
         }
-        if (!live) {  // keeps the arithmetic of a row left out finite
+        if (__any_sync(0xffffffffu, !live)) {  // keeps the arithmetic of a row left out finite
 #pragma unroll
             for (int j = 0; j < C; ++j)
-                v[j] = 0.0f;
+                v[j] = live ? v[j] : 0.0f;
         }
         float lse;
         const float s = row_softmax<LPR>(v, lse);
         const float inv = live ? __fdividef(1.0f, s) : 0.0f;
 #pragma unroll
-        for (int j = 0; j < C; ++j)
-            acc[j] = fmaf(v[j], inv, acc[j]);
+        for (int j = 0; j < C; j += 2)
+            fma2(Pair(v[j], v[j + 1]), Pair(inv, inv), Pair(acc[j], acc[j + 1]))
+                .get(acc[j], acc[j + 1]);
         lse = live ? lse : 0.0f;
         bad_logit |= !isfinite(lse);
         zsum = fmaf(lse, lse, zsum);
@@ -372,7 +434,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int j = 0; j < C; ++j) {
         const int c = Slice::col(l, j);
-        f[j] = c < E ? (float)counts[c] * inv_mk : 0.0f;
+        f[j] = c < E ? a * ((float)counts[c] * inv_mk) : 0.0f;  // a f_e
     }
     const int64_t stride = (int64_t)(gridDim.x * 256 / 32) * GW;
     for (int64_t base = (int64_t)warp * GW; base < N; base += stride) {
@@ -380,24 +442,33 @@ __global__ void __launch_bounds__(256)
         const bool inside = t < N, live = inside && (!mask || mask[t]);
         float v[C];
         Slice::load(logits + (inside ? t : 0) * E, inside ? E : 0, l, v);
-        if (!live) {
+        const bool any_out = __any_sync(0xffffffffu, !live);
+        if (any_out) {
 #pragma unroll
             for (int j = 0; j < C; ++j)
-                v[j] = 0.0f;
+                v[j] = live ? v[j] : 0.0f;
         }
         float lse;
         const float s = row_softmax<LPR>(v, lse);
-        float dot = 0.0f;
+        Pair dot2(0.0f, 0.0f);
 #pragma unroll
-        for (int j = 0; j < C; ++j)
-            dot += f[j] * v[j];
-        dot = row_sum<LPR>(dot);
+        for (int j = 0; j < C; j += 2)
+            dot2 = fma2(Pair(f[j], f[j + 1]), Pair(v[j], v[j + 1]), dot2);
+        float dot, dot1;
+        dot2.get(dot, dot1);
+        dot = row_sum<LPR>(dot + dot1);
         const float inv = __fdividef(1.0f, s);
         // p (a (f - inner) + b lse) = e (a f + c) / sum
-        const float c = b * lse - a * dot * inv;
+        const float c = b * lse - dot * inv;
 #pragma unroll
-        for (int j = 0; j < C; ++j)
-            v[j] = live ? v[j] * inv * (a * f[j] + c) : 0.0f;
+        for (int j = 0; j < C; j += 2)
+            mul2(mul2(Pair(v[j], v[j + 1]), Pair(inv, inv)), add2(Pair(f[j], f[j + 1]), Pair(c, c)))
+                .get(v[j], v[j + 1]);
+        if (any_out) {
+#pragma unroll
+            for (int j = 0; j < C; ++j)
+                v[j] = live ? v[j] : 0.0f;
+        }
         if (inside)
             Slice::store(dlogits + t * E, E, l, v);
     }
