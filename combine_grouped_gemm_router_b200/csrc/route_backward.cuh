@@ -359,6 +359,10 @@ struct DwArgs {
     int chunks;      // chunks of kChunk tokens
     int parts;       // equal shares of the chunks, one CTA each for every tile
     int x_boxes;     // tm_x is [d / 64][N][64] (d % 64 == 0), else [N][d]
+    // launched behind dx's kernel, which lets this one start once it has seen the planes complete:
+    // no wait for dx before the work, so CTAs take the SMs that dx leaves one by one. The wait
+    // comes at the end: what follows on the stream finds dx complete too.
+    int after_dx;
     const uint8_t *mask;
     float *part;     // [tiles][groups][parts][columns / 8][128 rows][8]
     uint64_t timeout_ns;
@@ -419,8 +423,8 @@ __global__ void __launch_bounds__(kDwThreads, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    grid_go();
-    grid_wait();  // the planes of the kernel before
+    if (!a.after_dx)
+        grid_wait();  // the planes of the kernel before
     gg::tc_fence_before();
     __syncthreads();
     gg::tc_fence_after();
@@ -640,6 +644,8 @@ __global__ void __launch_bounds__(kDwThreads, 1)
     if (warp == 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
                      : "memory");
+    if (a.after_dx)
+        grid_wait();
 }
 
 struct SumArgs {
@@ -996,8 +1002,8 @@ __global__ void __launch_bounds__((DxTile<BF16, false, ADD>::THREADS), 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    grid_go();
     grid_wait();  // the planes of the kernel before
+    grid_go();    // not earlier: dWr's kernel takes its start for the planes being there
     gg::tc_fence_before();
     __syncthreads();
     gg::tc_fence_after();
@@ -1196,8 +1202,8 @@ __global__ void __launch_bounds__((DxTile<BF16, true, ADD>::THREADS), 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
-    grid_go();
     grid_wait();  // the planes of the kernel before
+    grid_go();    // not earlier: dWr's kernel takes its start for the planes being there
     gg::tc_fence_before();
     gg::cluster_sync_all();  // barriers initialised in both CTAs before any remote use
     gg::tc_fence_after();
