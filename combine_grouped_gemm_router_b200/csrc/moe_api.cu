@@ -1451,7 +1451,7 @@ moe_status_t launch_router_dx(const moe_shape_t *s, const uint16_t *dl, const ui
 
 moe_status_t launch_router_dw(const moe_shape_t *s, const DwGeometry &g, const uint16_t *x,
                               const uint16_t *dl, const uint8_t *mask, float *part,
-                              bool after_dx, cudaStream_t st)
+                              cudaStream_t st)
 {
     const cuuint64_t N = (cuuint64_t)s->N, d = (cuuint64_t)s->d, E = (cuuint64_t)s->E;
     const cuuint64_t pitch = (cuuint64_t)dl_pitch_of(s);
@@ -1462,8 +1462,8 @@ moe_status_t launch_router_dw(const moe_shape_t *s, const DwGeometry &g, const u
     const cuuint64_t dl_pitch[3] = {pitch * 2, 128, N * pitch * 2};
     const cuuint64_t x_dims[2] = {d, N}, x_pitch[1] = {d * 2};
     const cuuint64_t xb_dims[3] = {64, N, d / 64}, xb_pitch[2] = {d * 2, 128};
-    const rb::DwArgs a{s->N, s->d, s->E, g.tiles, g.groups, g.chunks, g.parts, x_boxes, after_dx, mask,
-                       part, kWaitTimeoutNs};
+    const rb::DwArgs a{s->N, s->d, s->E, g.tiles, g.groups, g.chunks, g.parts, x_boxes, mask, part,
+                       kWaitTimeoutNs};
     auto go = [&](auto fold) {
         using T = rb::DwTile<decltype(fold)::value>;
         auto kern = rb::router_dw_kernel<decltype(fold)::value>;
@@ -1558,7 +1558,7 @@ moe_status_t route_backward_impl(const moe_shape_t *s, const RouteBackward &a, c
         rc = bf16 ? (a.dx_add ? go(yes, yes) : go(yes, no)) : (a.dx_add ? go(no, yes) : go(no, no));
     }
     if (rc == MOE_OK && a.dw)
-        rc = launch_router_dw(s, g, a.x, dl, a.mask, part, a.dx != nullptr, st);
+        rc = launch_router_dw(s, g, a.x, dl, a.mask, part, st);
     if (rc != MOE_OK || (!a.dw && !a.dbias))
         return rc;
     rb::SumArgs sum = {};

@@ -359,10 +359,6 @@ struct DwArgs {
     int chunks;      // chunks of kChunk tokens
     int parts;       // equal shares of the chunks, one CTA each for every tile
     int x_boxes;     // tm_x is [d / 64][N][64] (d % 64 == 0), else [N][d]
-    // launched behind dx's kernel, which lets this one start once it has seen the planes complete:
-    // no wait for dx before the work, so CTAs take the SMs that dx leaves one by one. The wait
-    // comes at the end: what follows on the stream finds dx complete too.
-    int after_dx;
     const uint8_t *mask;
     float *part;     // [tiles][groups][parts][columns / 8][128 rows][8]
     uint64_t timeout_ns;
@@ -423,8 +419,11 @@ __global__ void __launch_bounds__(kDwThreads, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    if (!a.after_dx)
-        grid_wait();  // the planes of the kernel before
+    grid_go();
+    // The planes are the work of the kernel before dx's: nothing but this wait says that they can be
+    // seen here (dx's having waited for them says so to dx's blocks only), so dWr's loads start
+    // when dx is done, and only its setup overlaps dx's end.
+    grid_wait();
     gg::tc_fence_before();
     __syncthreads();
     gg::tc_fence_after();
@@ -644,8 +643,6 @@ __global__ void __launch_bounds__(kDwThreads, 1)
     if (warp == 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
                      : "memory");
-    if (a.after_dx)
-        grid_wait();
 }
 
 struct SumArgs {
@@ -1002,8 +999,8 @@ __global__ void __launch_bounds__((DxTile<BF16, false, ADD>::THREADS), 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    grid_go();
     grid_wait();  // the planes of the kernel before
-    grid_go();    // not earlier: dWr's kernel takes its start for the planes being there
     gg::tc_fence_before();
     __syncthreads();
     gg::tc_fence_after();
@@ -1202,8 +1199,8 @@ __global__ void __launch_bounds__((DxTile<BF16, true, ADD>::THREADS), 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
+    grid_go();
     grid_wait();  // the planes of the kernel before
-    grid_go();    // not earlier: dWr's kernel takes its start for the planes being there
     gg::tc_fence_before();
     gg::cluster_sync_all();  // barriers initialised in both CTAs before any remote use
     gg::tc_fence_after();
