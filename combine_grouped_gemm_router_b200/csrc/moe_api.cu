@@ -1291,7 +1291,7 @@ struct RouteBackward {
 
 // Workspace of the router's backward pass.
 struct RouteBackLayout {
-    size_t dl, wp, bias, part, total;
+    size_t dl, dl16, row_exp, wp, box_exp, bias, part, total;
 };
 
 // dWr's tiles: 256 columns of x by 128 experts (or 64, folded); each tile's 128-token chunks in
@@ -1343,15 +1343,22 @@ RouteBackLayout route_back_layout(const moe_shape_t *s)
     size_t o = 0;
     if (rb::block_path(s->N, s->E, s->d)) {
         const size_t parts = (size_t)block_parts(s);
-        L.dl = L.wp = L.bias = 0;
+        L.dl = L.dl16 = L.row_exp = L.wp = L.box_exp = L.bias = 0;
         L.part = align_up(parts * s->E * 4);
         L.total = L.part + align_up(parts * s->E * s->d * 4);
         return L;
     }
     L.dl = o;
     o = align_up(o + 3 * (size_t)s->N * pitch * 2);
+    const bool bf16 = (s->flags & MOE_FLAG_OUT_BF16) != 0;  // dx from fp16 terms
+    L.dl16 = o;
+    o = align_up(o + (bf16 ? 2 * (size_t)s->N * pitch * 2 : 0));
+    L.row_exp = o;
+    o = align_up(o + (bf16 ? (size_t)s->N * 4 : 0));
     L.wp = o;
     o = align_up(o + 3 * (size_t)s->E * ((s->d + 63) / 64 * 64) * 2);
+    L.box_exp = o;
+    o = align_up(o + (size_t)((s->d + 63) / 64) * 4);
     L.bias = o;
     o = align_up(o + (size_t)split_blocks(s) * s->E * 4);
     L.part = o;
@@ -1377,15 +1384,16 @@ bool make_tmap_box(CUtensorMap *m, CUtensorMapDataType dt, int rank, const void 
 
 template <bool BF16, bool PAIR, bool ADD>
 moe_status_t launch_router_dx(const moe_shape_t *s, const uint16_t *dl, const uint16_t *wp,
-                              const uint16_t *add, void *dx, cudaStream_t st)
+                              const int32_t *row_exp, const int32_t *box_exp, const uint16_t *add,
+                              void *dx, cudaStream_t st)
 {
     using T = rb::DxTile<BF16, PAIR, ADD>;
     const cuuint64_t N = (cuuint64_t)s->N, d = (cuuint64_t)s->d, E = (cuuint64_t)s->E;
     const cuuint64_t pitch = (cuuint64_t)dl_pitch_of(s);
     CUtensorMap t_dl, t_w, t_dl1, t_w1, t_dx, t_add;
-    const cuuint64_t dl_dims[3] = {E, N, 3}, dl_pitch[2] = {pitch * 2, N * pitch * 2};
+    const cuuint64_t dl_dims[3] = {E, N, T::PLANES}, dl_pitch[2] = {pitch * 2, N * pitch * 2};
     const cuuint64_t wb = (d + 63) / 64;  // boxes of columns
-    const cuuint64_t w_dims[4] = {64, E, wb, 3}, w_pitch[3] = {128, E * 128, wb * E * 128};
+    const cuuint64_t w_dims[4] = {64, E, wb, T::PLANES}, w_pitch[3] = {128, E * 128, wb * E * 128};
     const cuuint64_t x_dims[2] = {d, N}, dx_pitch[1] = {d * (BF16 ? 2 : 4)}, add_pitch[1] = {d * 2};
     int nb = (int)wb < T::NB ? (int)wb : T::NB;
     if (PAIR)
@@ -1395,9 +1403,10 @@ moe_status_t launch_router_dx(const moe_shape_t *s, const uint16_t *dl, const ui
     const cuuint32_t dl1_box[3] = {32, 128, 1}, w1_box[4] = {64, 32, (cuuint32_t)(nb / 2), 1};
     const cuuint32_t p_box[2] = {(cuuint32_t)T::CP, 32};
     const CUtensorMapDataType b16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const CUtensorMapDataType terms = BF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : b16;
     const CUtensorMapSwizzle sw128 = CU_TENSOR_MAP_SWIZZLE_128B, sw64 = CU_TENSOR_MAP_SWIZZLE_64B;
-    if (!make_tmap_box(&t_dl, b16, 3, dl, dl_dims, dl_pitch, dl_box, PAIR ? sw64 : sw128) ||
-        !make_tmap_box(&t_w, b16, 4, wp, w_dims, w_pitch, w_box, sw128) ||
+    if (!make_tmap_box(&t_dl, terms, 3, dl, dl_dims, dl_pitch, dl_box, PAIR ? sw64 : sw128) ||
+        !make_tmap_box(&t_w, terms, 4, wp, w_dims, w_pitch, w_box, sw128) ||
         !make_tmap_box(&t_dx, BF16 ? b16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, dx, x_dims,
                        dx_pitch, p_box, sw128) ||
         (ADD && !make_tmap_box(&t_add, b16, 2, add, x_dims, add_pitch, p_box,
@@ -1421,6 +1430,8 @@ moe_status_t launch_router_dx(const moe_shape_t *s, const uint16_t *dl, const ui
     const int rows = PAIR ? 256 : 128;
     a.tiles = (s->N + rows - 1) / rows;
     const int fixed = T::weights(nb) + T::SLOT_AREA + 1024 + 512;
+    a.row_exp = row_exp;
+    a.box_exp = box_exp;
     a.units = (rb::kDxMaxSmem - fixed) / T::unit(nb);
     if (a.units > rb::kDxMaxUnits)
         a.units = rb::kDxMaxUnits;
@@ -1531,27 +1542,40 @@ moe_status_t route_backward_impl(const moe_shape_t *s, const RouteBackward &a, c
     }
     const RouteBackLayout L = route_back_layout(s);
     const DwGeometry g = dw_geometry(s);
+    const bool bf16 = (s->flags & MOE_FLAG_OUT_BF16) != 0, f16_terms = a.dx && bf16;
     uint16_t *dl = reinterpret_cast<uint16_t *>(ws + L.dl);
+    uint16_t *dl16 = reinterpret_cast<uint16_t *>(ws + L.dl16);
+    int32_t *row_exp = reinterpret_cast<int32_t *>(ws + L.row_exp);
     uint16_t *wp = reinterpret_cast<uint16_t *>(ws + L.wp);
+    int32_t *box_exp = reinterpret_cast<int32_t *>(ws + L.box_exp);
     float *bias = reinterpret_cast<float *>(ws + L.bias);
     float *part = reinterpret_cast<float *>(ws + L.part);
-    rb::SplitArgs sa{in, a.dx ? a.w_router : nullptr, s->N, s->E, s->K, s->d, dl_pitch_of(s), dl, wp, bias, split_blocks(s)};
+    // bf16 terms are read by dWr and by an fp32 dx
+    rb::SplitArgs sa{in, a.dx ? a.w_router : nullptr, s->N, s->E, s->K, s->d, dl_pitch_of(s),
+                     a.dw || (a.dx && !bf16) ? dl : nullptr, dl16, row_exp, wp, box_exp, bias,
+                     split_blocks(s)};
     int w_blocks = 0;
     if (a.dx) {
-        const int64_t want = ((int64_t)s->E * s->d / 8 + rb::kSplitThreads - 1) / rb::kSplitThreads;
+        const int64_t want = f16_terms ? (s->d + 63) / 64
+                                       : ((int64_t)s->E * s->d / 8 + rb::kSplitThreads - 1) /
+                                             rb::kSplitThreads;
         w_blocks = (int)(want < num_sms() ? want : num_sms());
     }
     row_lanes(s->E, [&](auto lpr) {
-        rb::router_split_grad_kernel<decltype(lpr)::value>
-            <<<sa.token_blocks + w_blocks, rb::kSplitThreads, 0, st>>>(sa);
+        constexpr int LPR = decltype(lpr)::value;
+        const auto kern = f16_terms ? rb::router_split_grad_kernel<LPR, true>
+                                    : rb::router_split_grad_kernel<LPR, false>;
+        kern<<<sa.token_blocks + w_blocks, rb::kSplitThreads, 0, st>>>(sa);
     });
     moe_status_t rc = launch_status();
     if (rc == MOE_OK && a.dx) {
-        const bool bf16 = (s->flags & MOE_FLAG_OUT_BF16) != 0;
         auto go = [&](auto b, auto add) {
             constexpr bool B = decltype(b)::value, A = decltype(add)::value;
-            return s->E <= 64 ? launch_router_dx<B, false, A>(s, dl, wp, a.dx_add, a.dx, st)
-                              : launch_router_dx<B, true, A>(s, dl, wp, a.dx_add, a.dx, st);
+            const uint16_t *terms = B ? dl16 : dl;
+            return s->E <= 64 ? launch_router_dx<B, false, A>(s, terms, wp, row_exp, box_exp,
+                                                              a.dx_add, a.dx, st)
+                              : launch_router_dx<B, true, A>(s, terms, wp, row_exp, box_exp,
+                                                             a.dx_add, a.dx, st);
         };
         const std::true_type yes;
         const std::false_type no;

@@ -6,14 +6,19 @@
 //   dx = dl Wr (+ dx_add)      dWr = dl^T x      dbias = sum_t dl
 // A masked token's dl is 0 whatever its inputs hold, and its row of x counts as zeros.
 //
-// The two contractions run on tcgen05 with bf16 operands and fp32 accumulation. x is bf16
-// already; the fp32 factors are split into bf16 terms, v = hi + mid + lo (each the rounding of
-// what is left: 3 x 8 significant bits hold all 24 of an fp32 value), and the products of the
-// terms are accumulated together:
-//   dWr: x (hi + mid + lo): exact products of the fp32 dl;
-//   dx, fp32: hi hi + hi mid + mid hi + mid mid + hi lo + lo hi (what is left out is below
-//       2^-23 of the product); bf16: hi hi + hi mid + mid hi (below 2^-14, against the output's
-//       own rounding of 2^-8).
+// The two contractions run on tcgen05 with 16-bit operands and fp32 accumulation. The fp32 factors
+// are split into terms, each the rounding of what is left, and the products of the terms are
+// accumulated together:
+//   dWr, beside a bf16 x: bf16 terms hi + mid + lo (3 x 8 significant bits hold all 24 of an fp32
+//       value): exact products of the fp32 dl;
+//   dx, fp32: the same terms of dl and Wr, hi hi + hi mid + mid hi + mid mid + hi lo + lo hi (what
+//       is left out is below 2^-23 of the product);
+//   dx, bf16: fp16 terms hi + lo (2 x 11 bits), hi hi + hi lo + lo hi: half the products. They too
+//       keep 2^-22 of a product: dl's entries sum to 0, so what the rows of Wr have in common
+//       drops out of dx, and an error that is small beside the products need not be small beside
+//       dx. fp16 has 5 exponent bits, so the terms are of dl 2^-r and Wr 2^-b, r per token and b
+//       per 64 columns of Wr such that the largest value lies in [2^14, 2^15): a value is off by at
+//       most 2^-23 of itself or 2^-39 of that largest one. The epilogue multiplies by 2^(r + b).
 // Four launches (one or two for little work, router_block_grad_kernel): the split
 // (router_split_grad_kernel), dx, dWr, and the sum of dWr's and dbias's partial results in a
 // fixed order; the middle two are scheduled while the one before them drains (grid_wait). No
@@ -65,6 +70,33 @@ __device__ __forceinline__ void split3x8(const float (&v)[8], uint4 (&out)[3])
 #pragma unroll
     for (int p = 0; p < 3; ++p)
         out[p] = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+}
+
+// Exponent x of values whose largest finite magnitude is `top`: top 2^-x in [2^14, 2^15), 0 if
+// there is none. Down to -127: what is scaled by more is below 2^-113.
+__device__ __forceinline__ int f16_terms_exp(float top)
+{
+    return top > 0.0f ? max((int)(__float_as_uint(top) >> 23) - 127 - 14, -127) : 0;
+}
+
+// |v|, 0 for an infinity or NaN.
+__device__ __forceinline__ float finite_abs(float v)
+{
+    v = fabsf(v);
+    return v <= 3.402823466e38f ? v : 0.0f;
+}
+
+// n values times `scale` -> their two fp16 terms. An infinity or NaN is the first one.
+template <int n>
+__device__ __forceinline__ void split_f16(const float (&v)[n], float scale, uint32_t (&w)[2][n / 2])
+{
+#pragma unroll
+    for (int i = 0; i < n / 2; ++i) {
+        const float a = v[2 * i] * scale, b = v[2 * i + 1] * scale;
+        w[0][i] = gg::pack_f16x2(a, b);
+        const float ra = a - f16_to_f32(w[0][i] & 0xFFFFu), rb = b - f16_to_f32(w[0][i] >> 16);
+        w[1][i] = gg::pack_f16x2(isfinite(a) ? ra : 0.0f, isfinite(b) ? rb : 0.0f);
+    }
 }
 
 // What the gradient of the logits is made of.
@@ -192,28 +224,83 @@ struct SplitArgs {
     const float *wr;  // nullable: no planes of the router weights wanted
     int N, E, K, d;
     int pitch;        // columns of a row of dl's planes, the ones past E zeros
-    uint16_t *dl;     // [3][N][pitch]
-    uint16_t *wp;     // [3][d / 64 rounded up][E][64]: a box of 64 columns of x in one piece
+    uint16_t *dl;     // bf16 terms, [3][N][pitch]; nullable
+    uint16_t *dl16;   // F16: fp16 terms of dl 2^-row_exp, [2][N][pitch]
+    int32_t *row_exp; // F16: [N]
+    // terms of the router weights, [d / 64 rounded up][E][64] each: a box of 64 columns of x in
+    // one piece. F16: two of fp16, of wr 2^-box_exp, else three of bf16
+    uint16_t *wp;
+    int32_t *box_exp; // F16: [d / 64 rounded up]
     float *bias_part; // [E][token_blocks]
     int token_blocks;
 };
 
 constexpr int kSplitThreads = 256;
 
-// Blocks [0, token_blocks): dl of their tokens, in planes, and its sum over them; LPR lanes per
-// token, 8 neighbouring columns each (one 16-byte store per plane). The other blocks: the
-// planes of the router weights.
-template <int LPR>
+// The last token_blocks blocks: dl of their tokens, in planes, and its sum over them; LPR lanes per
+// token, 8 neighbouring columns each (one 16-byte store per plane). The blocks before them: the
+// planes of the router weights (first, because fp16 terms take longer).
+// F16: the fp16 terms of a bf16 dx are wanted.
+template <int LPR, bool F16>
 __global__ void __launch_bounds__(kSplitThreads) router_split_grad_kernel(const SplitArgs a)
 {
     constexpr int GW = 32 / LPR, WARPS = kSplitThreads / 32;
     const int tid = threadIdx.x;
     grid_go();
-    if ((int)blockIdx.x >= a.token_blocks) {
+    const int w_blocks = (int)gridDim.x - a.token_blocks;
+    if (F16 && (int)blockIdx.x < w_blocks) {
+        __shared__ float s_top[WARPS];
+        const int boxes = (a.d + 63) / 64;
+        constexpr int NI = LPR < 2 ? 1 : LPR / 2;  // E <= 8 LPR: a thread's quarter rows of a box
+        for (int box = blockIdx.x; box < boxes; box += w_blocks) {
+            const float *src = a.wr + box * 64;
+            const int c = 4 * (tid & 15), c_end = a.d - box * 64;  // a multiple of 8
+            float4 q[NI];
+            float top = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int e = (tid >> 4) + i * (kSplitThreads / 16);
+                q[i] = e < a.E && c < c_end
+                           ? *reinterpret_cast<const float4 *>(src + (size_t)e * a.d + c)
+                           : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+                top = fmaxf(top, fmaxf(fmaxf(finite_abs(q[i].x), finite_abs(q[i].y)),
+                                       fmaxf(finite_abs(q[i].z), finite_abs(q[i].w))));
+            top = row_max<32>(top);
+            __syncthreads();  // the box before is done with
+            if ((tid & 31) == 0)
+                s_top[tid >> 5] = top;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w)
+                top = fmaxf(top, s_top[w]);
+            const int x = f16_terms_exp(top);
+            const float scale = pow2f(-x);
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int e = (tid >> 4) + i * (kSplitThreads / 16);
+                const float v[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+                uint32_t w[2][2];
+                split_f16<4>(v, scale, w);
+                if (e < a.E && c < c_end) {
+#pragma unroll
+                    for (int p = 0; p < 2; ++p)
+                        *reinterpret_cast<uint2 *>(
+                            a.wp + (((size_t)p * boxes + box) * a.E + e) * 64 + c) =
+                            make_uint2(w[p][0], w[p][1]);
+                }
+            }
+            if (tid == 0)
+                a.box_exp[box] = x;
+        }
+        return;
+    }
+    if ((int)blockIdx.x < w_blocks) {
         const int64_t n = (int64_t)a.E * a.d / 8;  // d % 8 == 0
-        const int64_t step = (int64_t)(gridDim.x - a.token_blocks) * kSplitThreads;
-        for (int64_t i = (int64_t)(blockIdx.x - a.token_blocks) * kSplitThreads + tid; i < n;
-             i += step) {
+        const int64_t step = (int64_t)w_blocks * kSplitThreads;
+        for (int64_t i = (int64_t)blockIdx.x * kSplitThreads + tid; i < n; i += step) {
             const float4 lo = reinterpret_cast<const float4 *>(a.wr)[2 * i];
             const float4 hi = reinterpret_cast<const float4 *>(a.wr)[2 * i + 1];
             const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
@@ -235,19 +322,38 @@ __global__ void __launch_bounds__(kSplitThreads) router_split_grad_kernel(const 
     const size_t plane = (size_t)a.N * a.pitch;
     float sum[8] = {};
     const int64_t stride = (int64_t)a.token_blocks * WARPS * GW;
-    for (int64_t t0 = ((int64_t)blockIdx.x * WARPS + warp) * GW; t0 < a.N; t0 += stride) {
+    const int block = (int)blockIdx.x - w_blocks;
+    for (int64_t t0 = ((int64_t)block * WARPS + warp) * GW; t0 < a.N; t0 += stride) {
         const int64_t t = t0 + grp;
         float v[8];
         token_dlogits<LPR>(a.in, a.N, E, a.K, t, l, s_row + warp * 256 + grp * (8 * LPR), v);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             sum[j] += v[j];
-        if (t < a.N && c0 < a.pitch) {
+        const bool stored = t < a.N && c0 < a.pitch;
+        if (a.dl && stored) {
             uint4 out[3];
             split3x8(v, out);
 #pragma unroll
             for (int p = 0; p < 3; ++p)
                 *reinterpret_cast<uint4 *>(a.dl + p * plane + t * a.pitch + c0) = out[p];
+        }
+        if constexpr (F16) {
+            float top = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                top = fmaxf(top, finite_abs(v[j]));
+            const int x = f16_terms_exp(row_max<LPR>(top));
+            uint32_t w[2][4];
+            split_f16<8>(v, pow2f(-x), w);
+            if (stored) {
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+                    *reinterpret_cast<uint4 *>(a.dl16 + p * plane + t * a.pitch + c0) =
+                        make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+                if (l == 0)
+                    a.row_exp[t] = x;
+            }
         }
     }
     __syncwarp();
@@ -268,7 +374,7 @@ __global__ void __launch_bounds__(kSplitThreads) router_split_grad_kernel(const 
 #pragma unroll
         for (int w = 0; w < WARPS; ++w)
             s += s_sum[w * (LPR * 8) + tid];
-        a.bias_part[(size_t)tid * a.token_blocks + blockIdx.x] = s;
+        a.bias_part[(size_t)tid * a.token_blocks + block] = s;
     }
 }
 
@@ -303,10 +409,11 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t 
            ((uint64_t)(1024u >> 4) << 32) | ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
 }
 
-// bf16 operands, fp32 accumulate; which operand is the M- or N-contiguous kind.
-__host__ __device__ constexpr uint32_t idesc(int M, int N, bool a_mn, bool b_mn)
+// bf16 (or both fp16) operands, fp32 accumulate; which operand is the M- or N-contiguous kind.
+__host__ __device__ constexpr uint32_t idesc(int M, int N, bool a_mn, bool b_mn, bool f16 = false)
 {
-    return gg::instr_desc_bf16(M, N) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16);
+    return (f16 ? gg::instr_desc_f16(M, N) : gg::instr_desc_bf16(M, N)) | ((uint32_t)a_mn << 15) |
+           ((uint32_t)b_mn << 16);
 }
 
 // One lane of a converged warp.
@@ -746,7 +853,7 @@ constexpr int kDxMaxSmem = 231424;
 
 template <bool BF16, bool PAIR, bool ADD>
 struct DxTile {
-    static constexpr int PLANES = BF16 ? 2 : 3;
+    static constexpr int PLANES = BF16 ? 2 : 3;                // fp16 terms, bf16 terms
     static constexpr int EW = 8;                               // epilogue warps
     static constexpr int THREADS = 32 * (2 + EW);
     // pieces of a warp in flight. fp32, up to 64 experts: two and 256 columns a slice, with
@@ -773,6 +880,7 @@ struct DxArgs {
     int slices;     // column slices
     int tiles;      // token tiles of 128 (pairs: 256)
     int units;      // ring units
+    const int32_t *row_exp, *box_exp;  // bf16 dx: the exponents of its factors (SplitArgs)
     uint64_t timeout_ns;
 };
 
@@ -836,7 +944,26 @@ __device__ __forceinline__ void dx_epilogue(const DxArgs &a, uint32_t tmem, uint
     int acc = 0;
     uint32_t acc_phase = 0;
     int ok = 1;
+    // bf16: exponents of this lane's row in the warp's pieces of a tile, loaded a tile ahead
+    static_assert(!BF16 || T::NB <= 2 * TURNS, "box exponents of a warp");
+    int row_x = 0, box_x[2] = {0, 0};
+    auto load_exps = [&](int n) {
+        if (!BF16 || n >= mine)
+            return;
+        int tile, slice;
+        item(n, tile, slice);
+        const int row = tile * 128 + q * 32 + lane, boxes = (a.d + 63) / 64;
+        row_x = row < a.N ? __ldcg(a.row_exp + row) : 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int box = slice * nb + i * TURNS + turn;
+            box_x[i] = i < own && box < boxes ? __ldcg(a.box_exp + box) : 0;
+        }
+    };
+    load_exps(0);
     for (int n = 0; n < mine && ok; ++n) {
+        const int exps[2] = {row_x + box_x[0], row_x + box_x[1]};
+        load_exps(n + 1);
         if (lane == 0)
             ok = gg::mbar_wait(tfull(acc), acc_phase, abort_flag, a.timeout_ns) ? 1 : 0;
         ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -865,6 +992,28 @@ __device__ __forceinline__ void dx_epilogue(const DxArgs &a, uint32_t tmem, uint
             gg::tmem_ld_wait();
             if (!ok)
                 break;
+            float scale = 1.0f;
+            if constexpr (BF16) {  // 2^(r + b), in two factors where one cannot hold it
+                const int x = exps[pc ? 1 : 0], x0 = max(-126, min(127, x));
+                scale = pow2f(x0);
+                if (__any_sync(0xffffffffu, x != x0)) {
+                    const float rest = pow2f(max(-126, min(127, x - x0)));
+#pragma unroll
+                    for (int c = 0; c < CP; ++c)
+                        v[c] = __float_as_uint(__uint_as_float(v[c]) * rest);
+                }
+                if constexpr (!ADD) {
+#pragma unroll
+                    for (int c = 0; c < CP; c += 2) {
+                        float lo, hi;
+                        mul2(Pair(__uint_as_float(v[c]), __uint_as_float(v[c + 1])),
+                             Pair(scale, scale))
+                            .get(lo, hi);
+                        v[c] = __float_as_uint(lo);
+                        v[c + 1] = __float_as_uint(hi);
+                    }
+                }
+            }
             if constexpr (ADD) {
 #pragma unroll
                 for (int c = 0; c < CP / 8; ++c) {
@@ -878,10 +1027,13 @@ __device__ __forceinline__ void dx_epilogue(const DxArgs &a, uint32_t tmem, uint
                                  : "r"(at));
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        v[8 * c + 2 * j] = __float_as_uint(
-                            __uint_as_float(v[8 * c + 2 * j]) + bf16_lo(x[j]));
-                        v[8 * c + 2 * j + 1] = __float_as_uint(
-                            __uint_as_float(v[8 * c + 2 * j + 1]) + bf16_hi(x[j]));
+                        float lo, hi;  // times scale (1 for an fp32 dx) plus dx_add
+                        fma2(Pair(__uint_as_float(v[8 * c + 2 * j]),
+                                  __uint_as_float(v[8 * c + 2 * j + 1])),
+                             Pair(scale, scale), Pair(bf16_lo(x[j]), bf16_hi(x[j])))
+                            .get(lo, hi);
+                        v[8 * c + 2 * j] = __float_as_uint(lo);
+                        v[8 * c + 2 * j + 1] = __float_as_uint(hi);
                     }
                 }
                 if (!BF16 && lane == 0)  // the slot's last store has read it
@@ -1042,7 +1194,7 @@ __global__ void __launch_bounds__((DxTile<BF16, false, ADD>::THREADS), 1)
         }
     } else if (warp == 1) {
         if (elect_one()) {
-            const uint32_t id = idesc(128, 64 * nb, false, true);
+            const uint32_t id = idesc(128, 64 * nb, false, true, BF16);
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = gg::mbar_wait(wfull, 0, abort_flag, a.timeout_ns);
@@ -1128,7 +1280,7 @@ __device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const CUtensorMap
 }
 
 // A stage of a tile (chunk = 32 experts). Products of two planes i, j: those below fp32's
-// rounding, i + j >= PLANES, are left out. bf16 dx: stage u holds both planes of chunk u and
+// rounding, i + j >= PLANES, are left out. bf16 dx: stage u holds both fp16 planes of chunk u and
 // gives all three products. fp32 dx: stages 0 .. C-1 hold the three planes of a chunk and give the
 // five products below hi hi; the stages after them hold the hi planes of three chunks each and
 // give hi hi. So the accumulator, which the tensor core truncates at every step, holds small
@@ -1258,7 +1410,7 @@ __global__ void __launch_bounds__((DxTile<BF16, true, ADD>::THREADS), 1)
     } else if (warp == 1) {
         if (rank == 0 && elect_one()) {
             // ---------------- MMA (first CTA of the pair)
-            const uint32_t id = idesc(256, 64 * a.nb, false, true);
+            const uint32_t id = idesc(256, 64 * a.nb, false, true, BF16);
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true;

@@ -579,8 +579,10 @@ size_t moe_route_backward_workspace_size(const moe_shape_t *shape);
  * may be NULL, not all three; dx may not overlap x (MOE_ERR_INVALID_ARG). N = 0 writes zero
  * weight gradients. N <= 2^30.
  * Precision: dl and the fp32 outputs as fp32 sums (the tensor cores run on bf16 terms of the
- * fp32 factors, three of each: nothing of dl is lost); a bf16 dx to 2^-14 before its own
- * rounding. The same bits every run. A non-finite gradient, weight or (unmasked) hidden state
+ * fp32 factors, three of each: nothing of dl is lost). A bf16 dx is a sum of the same precision,
+ * rounded once, from fp16 terms, two of each factor: a factor is within 2^-23 of itself or 2^-39
+ * of the largest of its token (dl) or of its columns 64 j to 64 j + 63 (w_router), if that is
+ * more. The same bits every run. A non-finite gradient, weight or (unmasked) hidden state
  * gives non-finite results where it enters; an infinity may arrive as NaN.
  * ws as for moe_balance_loss, moe_route_backward_workspace_size bytes. */
 moe_status_t moe_route_backward(const moe_shape_t *shape, const uint16_t *x,
