@@ -383,13 +383,24 @@ __host__ __device__ constexpr int epilogue_cols(int MODE)
 }
 
 // 32 values -> one block of the 8-bit checkpoint: 32 e4m3 codes at dst, the exponent byte j + 127
-// returned (the FP8 return payload's rule, see down_epilogue_fp8_return).
+// returned (the FP8 return payload's rule, see down_epilogue_fp8_return, for the finite values; the
+// payload saturates the others, here they are NaN codes and leave the block's exponent alone: a
+// gradient from a lost activation must not look like one from 448).
 __device__ __forceinline__ uint32_t checkpoint_block(const float *f, uint8_t *dst)
 {
     uint32_t mx = 0;
 #pragma unroll
     for (int k = 0; k < 32; ++k)
         mx = max(mx, __float_as_uint(f[k]) & 0x7FFFFFFFu);
+    const bool odd = mx >= 0x7F800000u;
+    if (odd) {
+        mx = 0;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+            const uint32_t a = __float_as_uint(f[k]) & 0x7FFFFFFFu;
+            mx = max(mx, a < 0x7F800000u ? a : 0u);
+        }
+    }
     const int j = e4m3_scale_exp(__uint_as_float(mx));
     const float inv = pow2f(-j);
     uint32_t p[8];
@@ -397,6 +408,12 @@ __device__ __forceinline__ uint32_t checkpoint_block(const float *f, uint8_t *ds
     for (int k = 0; k < 8; ++k)
         p[k] = pack_e4m3x2(f[4 * k] * inv, f[4 * k + 1] * inv) |
                (pack_e4m3x2(f[4 * k + 2] * inv, f[4 * k + 3] * inv) << 16);
+    if (odd) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+            if ((__float_as_uint(f[k]) & 0x7FFFFFFFu) >= 0x7F800000u)
+                p[k / 4] |= 0x7Fu << (8 * (k & 3));
+    }
     reinterpret_cast<uint4 *>(dst)[0] = make_uint4(p[0], p[1], p[2], p[3]);
     reinterpret_cast<uint4 *>(dst)[1] = make_uint4(p[4], p[5], p[6], p[7]);
     return (uint32_t)(j + 127);

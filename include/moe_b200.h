@@ -601,6 +601,9 @@ size_t moe_checkpoint_bytes(const moe_shape_t *shape);
  * codes with one power of two per 32 columns, the block rule of MOE_FLAG_FP8_RETURN. Row r of
  * ckpt (stride 2f + roundup16(f / 16) bytes): f codes of g, f codes of u, f / 32 exponent bytes
  * j + 127 of g, f / 32 of u; padding bytes and rows past offsets[E] are left as they were.
+ * A g or u that is infinite or NaN is saved as e4m3's NaN and left out of its block's power of two
+ * (the payload saturates instead), so moe_swiglu_backward's results from it are NaN too; it is
+ * reported as moe_expert_up reports it (MOE_ERR_F16_RANGE with fp16 h, not at all with bf16 h).
  * h is moe_expert_up's, bit for bit. */
 moe_status_t moe_expert_up_checkpoint(const moe_shape_t *shape, const uint16_t *x_sorted,
                                       const int32_t *offsets, const uint16_t *w1,
