@@ -430,10 +430,13 @@ def moe_affinity_accumulate(N, E, K, topk_j, topk_j1, counts, stream=None):
 def _args(where, stream, *wanted):
     """The addresses of tensors, after refusing (MoeError) one that the kernels would misread:
     each of ``wanted`` is (name, tensor, element types, least number of elements). None and raw
-    addresses pass. The last address is the stream's."""
+    addresses pass (not the workspace's: its size is told by the tensor). The last address is the
+    stream's."""
     device, out = -2, []
     for name, t, dtypes, least in wanted:
         if t is None or t.__class__ is int:
+            if t is not None and name == "ws":
+                raise MoeError(1, f"{where}: ws is a raw address, not a tensor")
             out.append(t)
             continue
         if t.dtype not in dtypes:

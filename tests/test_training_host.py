@@ -171,3 +171,12 @@ def test_references_against_differences():
     np.testing.assert_allclose(hh, act(gt, ut), rtol=1e-12)
     np.testing.assert_allclose(dg, dh * (act(gt + h, ut) - act(gt - h, ut)) / (2 * h), atol=1e-9)
     np.testing.assert_allclose(du, dh * (act(gt, ut + h) - act(gt, ut - h)) / (2 * h), atol=1e-9)
+
+
+def test_raw_workspace_address_is_refused(m):
+    """Other arguments may be addresses; a workspace's size has to be known."""
+    shape = m.make_shape(8, 128, 128, 8, 2, 1)
+    with pytest.raises(m.MoeError, match="moe_balance_loss: ws is a raw address"):
+        m.moe_balance_loss(shape, P, P, P, P, P, P, ws=P)
+    with pytest.raises(m.MoeError, match="moe_route_backward: ws is a raw address"):
+        m.moe_route_backward(shape, P, P, P, P, dlogits=P, ws=P)
