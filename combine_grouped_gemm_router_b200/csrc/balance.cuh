@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(256)
     const int64_t stride = (int64_t)(gridDim.x * 256 / 32) * GW;
     for (int64_t base = (int64_t)warp * GW; base < N; base += stride) {
         const int64_t t = base + grp;
-        const bool inside = t < N, live = inside && (!mask || mask[t]);
+        const bool inside = t < N, live = inside && M > 0 && (!mask || mask[t]);
         float v[C];
         Slice::load(logits + (inside ? t : 0) * E, inside ? E : 0, l, v);
         const bool any_out = __any_sync(0xffffffffu, !live);
