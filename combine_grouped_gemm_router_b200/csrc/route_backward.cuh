@@ -13,12 +13,13 @@
 //       value): exact products of the fp32 dl;
 //   dx, fp32: the same terms of dl and Wr, hi hi + hi mid + mid hi + mid mid + hi lo + lo hi (what
 //       is left out is below 2^-23 of the product);
-//   dx, bf16: fp16 terms hi + lo (2 x 11 bits), hi hi + hi lo + lo hi: half the products. They too
-//       keep 2^-22 of a product: dl's entries sum to 0, so what the rows of Wr have in common
-//       drops out of dx, and an error that is small beside the products need not be small beside
-//       dx. fp16 has 5 exponent bits, so the terms are of dl 2^-r and Wr 2^-b, r per token and b
-//       per 64 columns of Wr such that the largest value lies in [2^14, 2^15): a value is off by at
-//       most 2^-23 of itself or 2^-39 of that largest one. The epilogue multiplies by 2^(r + b).
+//   dx, bf16: fp16 terms hi + lo (2 x 11 bits), hi hi + hi lo + lo hi: half the products, and what
+//       is left out is below 2^-20 of the product. (Two bf16 terms lose 2^-16 of it. That is small
+//       beside the output's rounding, but not beside dx where products cancel: dl's entries sum
+//       to 0, so what the rows of Wr have in common drops out of dx.) fp16 has 5 exponent bits,
+//       so the terms are of dl 2^-r and Wr 2^-b, r per token and b per 64 columns of Wr such that
+//       the largest value lies in [2^14, 2^15): a value is off by at most 2^-22 of itself or
+//       2^-39 of that largest one. The epilogue multiplies by 2^(r + b).
 // Four launches (one or two for little work, router_block_grad_kernel): the split
 // (router_split_grad_kernel), dx, dWr, and the sum of dWr's and dbias's partial results in a
 // fixed order; the middle two are scheduled while the one before them drains (grid_wait). No

@@ -580,7 +580,7 @@ size_t moe_route_backward_workspace_size(const moe_shape_t *shape);
  * weight gradients. N <= 2^30.
  * Precision: dl and the fp32 outputs as fp32 sums (the tensor cores run on bf16 terms of the
  * fp32 factors, three of each: nothing of dl is lost). A bf16 dx is a sum of the same precision,
- * rounded once, from fp16 terms, two of each factor: a factor is within 2^-23 of itself or 2^-39
+ * rounded once, from fp16 terms, two of each factor: a factor is within 2^-22 of itself or 2^-39
  * of the largest of its token (dl) or of its columns 64 j to 64 j + 63 (w_router), if that is
  * more. The same bits every run. A non-finite gradient, weight or (unmasked) hidden state
  * gives non-finite results where it enters; an infinity may arrive as NaN.

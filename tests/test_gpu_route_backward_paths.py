@@ -72,11 +72,12 @@ def pair_gradients(N, d, E, seed):
                                    (2100, 392, 129), (1300, 264, 100), (700, 1032, 200)])
 def test_dx_of_cancelling_products(N, d, E, bf16):
     """dl's entries sum to 0 in a softmax's backward pass, so what all rows of Wr have in common
-    drops out of dx, but not the error made in its products. Both terms of an output need 24 bits
-    of each factor: six products of bf16 terms, of which at most two steps of 16 experts hold
-    something other than 0, so at most 12 truncated additions (2^-23 of at most the terms'
-    magnitudes each), with 2^-25 left out: 2^-19 of the magnitudes, beside the output's rounding. A
-    factor cut to its first two bf16 terms is off by up to 2^-17 of them."""
+    drops out of dx, but not the error made in its products. fp32 dx: six products of bf16 terms,
+    of which at most two steps of 16 experts hold something other than 0, so at most 12 truncated
+    additions (2^-23 of at most the terms' magnitudes each), with 2^-24 left out; bf16 dx: three
+    products of fp16 terms, 6 truncated additions, with 3 x 2^-22 left out (of each factor, and
+    the product of the small terms). Either is below 2^-19 of the magnitudes, beside the output's
+    rounding. A factor cut to its first two bf16 terms is off by up to 2^-17 of them."""
     m = lib()
     assert N * d * E > LITTLE_WORK
     a = pair_gradients(N, d, E, E)
@@ -94,7 +95,7 @@ def test_dx_of_cancelling_products(N, d, E, bf16):
                                         (700, 264, 256, True), (4099, 328, 40, False)])
 def test_dx_of_far_ranges(N, d, E, bf16):
     """Gradients and weights over 45 binades within a token and within 64 columns, tokens and
-    columns of very different size: a factor of a bf16 dx is within 2^-23 of itself or 2^-39 of the
+    columns of very different size: a factor of a bf16 dx is within 2^-22 of itself or 2^-39 of the
     largest of its token (dl) or its 64 columns (Wr), beside the 2^-17 of the terms that the
     accumulation may lose; results below fp32's normal range may be 0."""
     m = lib()
@@ -207,10 +208,10 @@ def full_mantissa(rng, *size):
 @pytest.mark.parametrize("N,d,E", [(1500, 512, 64), (9001, 264, 20), (2100, 392, 129),
                                    (1300, 264, 100), (700, 1032, 200)])
 def test_every_term_of_a_product_counts(N, d, E):
-    """One expert per token: an element of dx is one product, all of it: at most 6 products of terms
-    (12 truncated additions were they in two steps, 2^-23 of the result each) and 2^-25 left out,
-    2^-19 of the value. A factor without its third bf16 term is off by up to 2^-17, a product
-    without mid x mid by up to 2^-18. One token per expert: an element of dWr is one product of dl
+    """One expert per token: an element of dx is one product, all of it: 6 products of bf16 terms or
+    3 of fp16 terms (as many truncated additions, 2^-23 of the result each) and 2^-24 or 3 x 2^-22
+    left out, 2^-19 of the value. A factor without its third bf16 term is off by up to 2^-17, a
+    product without mid x mid by up to 2^-16. One token per expert: an element of dWr is one product of dl
     (three terms, two additions truncated and one rounded) and an exact bf16: 2^-21; without the
     third term up to 2^-17."""
     m = lib()
