@@ -14,8 +14,9 @@
 // columns a lane the shuffles were a third of the instructions. The sums (131072 x 256 with a
 // mask: 33 us, of which 4 in balance_finish_kernel) read the next row's logits while a row is
 // worked on; their loop streams at about 6 TB/s, the rest is the start and the end of the two
-// kernels. The gradient (30011 x 160: 11 us) is bound by issue slots: what can be done to two
-// columns by one instruction is (12 us one by one).
+// kernels. The gradient (30011 x 160: 10 us, its bytes 6) waits for memory: a row is loaded, worked
+// on and stored before the next one is loaded (issue slots half busy, 7 warps of an issue waiting
+// for loads), and the grid's 3.2 passes over the rows cost 4.
 #pragma once
 
 #include "common.cuh"

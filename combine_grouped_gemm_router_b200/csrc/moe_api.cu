@@ -1164,8 +1164,9 @@ moe_status_t combine_impl(const moe_shape_t *s, const void *y, const int32_t *ro
 
 // ---------------------------------------------------------------- training
 
-// Blocks of the balance sums: one per SM, and no more than give each warp a row. One block
-// takes a small call alone (and writes its outputs, without a second kernel).
+// Blocks of the balance sums: one per SM, but no more than one for every 8192 logits (above 146
+// experts these are fewer rows than a block's warps take at once, so that some warps have none).
+// One block takes a small call alone (and writes its outputs, without a second kernel).
 constexpr int64_t kBalSingle = 8192;  // logits of a call that one block takes
 
 int balance_blocks(const moe_shape_t *s)

@@ -438,7 +438,7 @@ __device__ __forceinline__ bool elect_one()
 // box of zeros. More experts: a CTA takes 128 of them. A chunk's sum is read back and added to
 // fp32 registers before it is longer than 128 tokens: the tensor core's accumulator truncates,
 // and a truncation per step over tens of thousands of tokens would cost the low bits that the
-// split keeps. 32768 x 4096 x 64, mask: 59 us, 4.8 TB/s, MMA 0.67 of it.
+// split keeps. 32768 x 4096 x 64, mask: 60 us, 4.8 TB/s, MMA 0.67 of it.
 // The CTAs of one share of the tokens walk over them together, one column tile each, so that
 // rows of x are read whole within a short time.
 constexpr int kChunk = 128;  // tokens accumulated in TMEM
@@ -841,12 +841,13 @@ __global__ void __launch_bounds__(256) router_sum_kernel(const SumArgs a)
 // j <= PLANES - 1 - i of the weights; eight epilogue warps. The CTAs of a group hold the column
 // slices of x and walk over the tokens together, so rows of dx are written whole within a
 // short time (measured against CTAs that each walk a strip of their own: 90 -> 74 us at
-// 32768 x 4096 x 64; 52 us now, 86 with dx_add: 541 MB at 6.2 TB/s).
+// 32768 x 4096 x 64; 55 us now, 88 with dx_add: 541 MB at 6.1 TB/s).
 // More experts (router_dx_pair_kernel): the weights' planes do not fit beside the rest, so both
 // operands stream, 32 experts a stage. A pair of CTAs computes 256 tokens x 256 columns
 // (cta_group::2): each loads its 128 tokens of dl and half of the columns of the weights, which
-// both read. Bound by those reads through L2 (about 40 bytes a cycle and SM): 64 us at
-// 16384 x 4096 x 128, 39 at 4001 x 7168 x 256 (fp32: 70).
+// both read. 4001 x 7168 x 256: 40 us, fp32 79 with the matrix pipe 0.7 busy over all; the tiles
+// are 6.05 rounds of the pairs there, so the last of 7 rounds keeps few of them busy. 8192 x
+// 2048 x 128: 20 us, 3.5 rounds paid as 4.
 constexpr int kUnit = 16384;   // 128 tokens x 64 experts, bf16
 constexpr int kPiece = 4096;   // 32 tokens x 128 bytes of dx: what one warp stores at a time
 constexpr int kDxMaxUnits = 6;

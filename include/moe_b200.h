@@ -562,7 +562,9 @@ moe_status_t moe_balance_loss_backward(const moe_shape_t *shape, const float *lo
                                        const int32_t *tokens, float balance_coef, float z_coef,
                                        const float *dloss, float *dlogits, moe_stream_t stream);
 
-/* Workspace bytes for moe_route_backward. 0 on an invalid shape. */
+/* Workspace bytes for moe_route_backward. 0 on an invalid shape. They depend on the number of SMs
+ * of the current device (as the grids do): ask with the device current that the call runs on; a
+ * workspace too small for it is refused. */
 size_t moe_route_backward_workspace_size(const moe_shape_t *shape);
 
 /* Backward pass of moe_route. With dl [N][E] the gradient of the logits,
@@ -576,8 +578,8 @@ size_t moe_route_backward_workspace_size(const moe_shape_t *shape);
  * dx [N][d] fp32, or bf16 with MOE_FLAG_OUT_BF16; dx_add [N][d] bf16, nullable (the gradient
  * that reaches x by other ways; a bf16 dx may alias it); a masked token's dx is dx_add or 0.
  * dw_router [E][d], dbias [E] fp32. Each of dx (with w_router), dw_router (with x) and dbias
- * may be NULL, not all three; dx may not overlap x (MOE_ERR_INVALID_ARG). N = 0 writes zero
- * weight gradients. N <= 2^30.
+ * may be NULL, not all three; with dw_router, dx may not overlap x (MOE_ERR_INVALID_ARG). N = 0
+ * writes zero weight gradients. N <= 2^30.
  * Precision: dl and the fp32 outputs as fp32 sums (the tensor cores run on bf16 terms of the
  * fp32 factors, three of each: nothing of dl is lost). A bf16 dx is a sum of the same precision,
  * rounded once, from fp16 terms, two of each factor: a factor is within 2^-22 of itself or 2^-39
