@@ -219,19 +219,19 @@ class ClockSampler:
 # summarised in profiles/.
 # A figure holds only for the kernel code it was measured on (kernel_source_hash of
 # grouped_gemm.cuh: comments and whitespace do not count).
-_UP_SHA = "5d9c986bcab4eb5e75d5a505601235db5f1094189b4665fedb8a52bf68bf5ea7"
+_UP_SHA = "e5a9d2ca69b9e8a079c5c750f91b94245c3d10bfd5792adf61995d80ac350322"
 MEASURED_UP_TRAFFIC = {
     # workload: (kernel source sha256, bytes per launch)
-    "mixtral_prefill": (_UP_SHA, 2 * (995.3e6 + 112.5e6)),      # half-size capture x 2
-    "mixtral_prefill_fp8": (_UP_SHA, 2 * (487.8e6 + 104.3e6)),  # half-size capture x 2
-    "e128_skew": (_UP_SHA, 894.8e6 + 34.7e6),
-    "e128_skew_fp8": (_UP_SHA, 444.1e6 + 32.6e6),
+    "mixtral_prefill": (_UP_SHA, 2 * (1010.5e6 + 111.7e6)),      # half-size capture x 2
+    "mixtral_prefill_fp8": (_UP_SHA, 2 * (488.0e6 + 105.6e6)),  # half-size capture x 2
+    "e128_skew": (_UP_SHA, 888.7e6 + 34.4e6),
+    "e128_skew_fp8": (_UP_SHA, 444.2e6 + 32.7e6),
     # the return payload changes the down GEMM and the combine, not the gate/up GEMM
-    "mixtral_prefill_fp8_return": (_UP_SHA, 2 * (487.8e6 + 104.3e6)),
-    "e128_skew_fp8_return": (_UP_SHA, 444.1e6 + 32.6e6),
-    "decode": (_UP_SHA, 6080.8e6 + 3.8e6),
-    "decode_fp8": (_UP_SHA, 3042.2e6 + 3.8e6),
-    "stack4": (_UP_SHA, 4041.5e6 + 597.3e6),                    # one layer's launch
+    "mixtral_prefill_fp8_return": (_UP_SHA, 2 * (488.0e6 + 105.6e6)),
+    "e128_skew_fp8_return": (_UP_SHA, 444.2e6 + 32.7e6),
+    "decode": (_UP_SHA, 6081.2e6 + 3.9e6),
+    "decode_fp8": (_UP_SHA, 3042.0e6 + 3.9e6),
+    "stack4": (_UP_SHA, 7823.0e6 + 595.4e6),  # one layer's launch, mean of six
 }
 
 
